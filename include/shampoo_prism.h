@@ -314,6 +314,38 @@ int shp_matmul_f64_ex(const double* A, const double* B, double* C, int64_t M, in
 /* hi = TF32(x) (round to nearest), lo = TF32(x - hi), for `count` floats. */
 int shp_split_tf32(const float* X, int64_t count, float* hi, float* lo, shp_stream stream);
 
+/* ---- Products of an expert layer (no counterpart on the pages). ----
+ *
+ * The weight blocks [groups][m][n] this library preconditions may be the
+ * experts of a layer whose rows (tokens) are sorted by expert: group e owns the
+ * rows offsets[e] .. offsets[e+1]-1 of a [T][...] matrix.  `offsets` is a
+ * DEVICE array of groups + 1 int64, non-decreasing and within 0..T; it is read
+ * by the kernels, nothing waits for the host, and any group may be empty.
+ * Offsets outside 0..T are clamped and a decreasing pair counts as an empty
+ * group, so no value of them reaches outside the operands.  Operands are bf16,
+ * sums fp32; K, N, m, n are multiples of 8; T and the groups' sizes are
+ * arbitrary.  groups <= 65535.  No workspace. */
+
+/* Y[t] = X[t] W[e(t)] for every row t of every group: the forward product of
+ * an expert layer, and with the other w_trans the gradient of its input.
+ * X: [T][K] bf16; W: [groups][K][N] bf16, or with w_trans = 1 [groups][N][K]
+ * (W[e]^T is applied); Y: [T][N], bf16 (out_storage = SHP_BF16) or fp32
+ * (SHP_TF32).  Rows of Y outside every group are left as they were.  A row of
+ * Y depends on its own row of X and its group's W alone.  Y may not alias X
+ * or W.  T = 0 launches nothing. */
+int shp_grouped_matmul(const void* X, const int64_t* offsets, const void* W, int w_trans, void* Y,
+                       int out_storage, int64_t T, int64_t K, int64_t N, int64_t groups,
+                       shp_stream stream);
+
+/* G[e] = A_e^T B_e over the rows of group e: the gradient of the weight blocks
+ * in the layout shampoo_gram_ema takes (A = X, B = dY for W stored [K][N];
+ * A = dY, B = X for W stored [N][K]).
+ * A: [T][m] bf16; B: [T][n] bf16; G: [groups][m][n] fp32.  accumulate = 1 adds
+ * to G (one rounding per element; subnormal results become zero).  An empty
+ * group's G is set to zero, or left as it is when accumulating. */
+int shp_grouped_wgrad(const void* A, const void* B, const int64_t* offsets, float* G, int64_t T,
+                      int64_t m, int64_t n, int64_t groups, int accumulate, shp_stream stream);
+
 /* Number of kernels this library has launched in the process so far
  * (host-side counter, all threads and devices). */
 uint64_t shp_kernel_launches(void);

@@ -36,6 +36,11 @@ struct Arena {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+// Row and column counts whose tile coordinates stay inside 32 bits.
+constexpr int64_t kMaxRows = INT32_MAX - 1024;
+
 bool opts_ok(const shp_prism_opts* o) {
   if (o == nullptr) return false;
   if (o->d != 1 && o->d != 2) return false;
@@ -447,7 +452,7 @@ const char* shp_version(void) { return "0.1.0"; }
 uint64_t shp_kernel_launches(void) {
   if (cudaDeviceSynchronize() != cudaSuccess) return 0;
   return kernel_runs_gemm() + kernel_runs_sketch() + kernel_runs_elementwise() +
-         kernel_runs_small() + kernel_runs_ozaki();
+         kernel_runs_small() + kernel_runs_ozaki() + kernel_runs_grouped();
 }
 
 int shp_split_tf32(const float* X, int64_t count, float* hi, float* lo, shp_stream stream) {
@@ -477,6 +482,35 @@ int shp_matmul(const void* A, const float* A_lo, int a_trans, const void* B, con
                     static_cast<int>(M), static_cast<int>(N), nullptr);
   CK(gemm_tc(mode, a, b, static_cast<int>(M), static_cast<int>(N), static_cast<int>(K),
              static_cast<int>(batch), e, static_cast<cudaStream_t>(stream)));
+  return SHP_OK;
+}
+
+int shp_grouped_matmul(const void* X, const int64_t* offsets, const void* W, int w_trans, void* Y,
+                       int out_storage, int64_t T, int64_t K, int64_t N, int64_t groups,
+                       shp_stream stream) {
+  if (!offsets || !W || T < 0 || K <= 0 || N <= 0 || groups <= 0) return SHP_EINVAL;
+  if (T > 0 && (!X || !Y)) return SHP_EINVAL;
+  if (out_storage != SHP_BF16 && out_storage != SHP_TF32) return SHP_EINVAL;
+  if (K % 8 || N % 8) return SHP_EINVAL;
+  if (!aligned16(X) || !aligned16(W) || !aligned16(Y) || !aligned8(offsets)) return SHP_EINVAL;
+  if (T > kMaxRows || K > kMaxRows || N > kMaxRows || groups > 65535) return SHP_EUNSUPPORTED;
+  if (T == 0) return SHP_OK;
+  CK(grouped_rows(X, offsets, W, w_trans != 0, Y, static_cast<int>(T), static_cast<int>(K),
+                  static_cast<int>(N), static_cast<int>(groups), out_storage == SHP_TF32,
+                  static_cast<cudaStream_t>(stream)));
+  return SHP_OK;
+}
+
+int shp_grouped_wgrad(const void* A, const void* B, const int64_t* offsets, float* G, int64_t T,
+                      int64_t m, int64_t n, int64_t groups, int accumulate, shp_stream stream) {
+  if (!offsets || !G || T < 0 || m <= 0 || n <= 0 || groups <= 0) return SHP_EINVAL;
+  if (T > 0 && (!A || !B)) return SHP_EINVAL;
+  if (m % 8 || n % 8) return SHP_EINVAL;
+  if (!aligned16(A) || !aligned16(B) || !aligned16(G) || !aligned8(offsets)) return SHP_EINVAL;
+  if (T > kMaxRows || m > kMaxRows || n > kMaxRows || groups > 65535) return SHP_EUNSUPPORTED;
+  CK(grouped_wgrad(A, B, offsets, G, static_cast<int>(T), static_cast<int>(m),
+                   static_cast<int>(n), static_cast<int>(groups), accumulate != 0,
+                   static_cast<cudaStream_t>(stream)));
   return SHP_OK;
 }
 

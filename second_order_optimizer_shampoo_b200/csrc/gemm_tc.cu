@@ -1238,6 +1238,12 @@ bool tensor_map_rows(CUtensorMap* m, const float* ptr, int64_t inner, int64_t ro
                   CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+bool tensor_map(CUtensorMap* m, const void* ptr, int esz, int64_t inner, int64_t rows,
+                int64_t batch, int64_t ld, int64_t bstride, int box_inner, int box_rows,
+                CUtensorMapSwizzle swz) {
+  return make_map(m, ptr, esz, inner, rows, batch, ld, bstride, box_inner, box_rows, swz);
+}
+
 cudaError_t gemm_tc(int mode, const Operand& A, const Operand& B, int M, int N, int K,
                     int batch, const EpiParams& ep, cudaStream_t st) {
   if (M <= 0 || N <= 0 || K <= 0 || batch <= 0) return cudaSuccess;

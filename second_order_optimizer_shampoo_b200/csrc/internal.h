@@ -112,6 +112,12 @@ cudaError_t gemm_tc(int mode, const Operand& A, const Operand& B, int M, int N, 
 bool tensor_map_rows(CUtensorMap* m, const float* ptr, int64_t inner, int64_t rows,
                      int64_t batch, int64_t ld, int64_t bstride, int box_inner, int box_rows);
 
+// The same for elements of 2 or 4 bytes (copied bit for bit) with the given
+// swizzle of the box in shared memory.
+bool tensor_map(CUtensorMap* m, const void* ptr, int esz, int64_t inner, int64_t rows,
+                int64_t batch, int64_t ld, int64_t bstride, int box_inner, int box_rows,
+                CUtensorMapSwizzle swz);
+
 // 4-D int8 map over [blocks][slices][rows][kb_bytes] (the K-blocked digit
 // slices of the Ozaki-scheme products, ozaki.cu; kb_bytes 64 or 128) with a
 // box of all slices x box_rows x kb_bytes and the swizzle of that row
@@ -365,6 +371,16 @@ cudaError_t oz_gform_d1(const double* R, int64_t n, int batch, const Ctl& ctl, d
 cudaError_t oz_finish(int64_t n, int batch, const Ctl& ctl, double c_exponent, const double* S,
                       float* X_out, bool z_slots, cudaStream_t st);
 uint64_t kernel_runs_ozaki();
+
+// ---- Products of rows grouped by expert (grouped.cu); bf16 operands
+// Y[t] = X[t] W_e (W: [groups][K][N]) or X[t] W_e^T (w_trans, W: [groups][N][K])
+// for the rows t of [offsets[e], offsets[e+1]); Y is bf16, or fp32 with f32.
+cudaError_t grouped_rows(const void* X, const int64_t* offsets, const void* W, bool w_trans,
+                         void* Y, int T, int K, int N, int groups, bool f32, cudaStream_t st);
+// G[e] (M x N) = A_e^T B_e over the rows of group e, or G[e] += with accumulate.
+cudaError_t grouped_wgrad(const void* A, const void* B, const int64_t* offsets, float* G, int T,
+                          int M, int N, int groups, bool accumulate, cudaStream_t st);
+uint64_t kernel_runs_grouped();
 
 
 }  // namespace shp

@@ -301,6 +301,72 @@ def shp_matmul(Amat, B, prec="tf32", a_trans=False, b_trans=False, A_lo=None, B_
     return out
 
 
+def _on_current(*ts):
+    """The tensors share the current CUDA device (calls go to its current stream)."""
+    dev = torch.device("cuda", torch.cuda.current_device())
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensor on {t.device}, but the current device is {dev}")
+
+
+def _want(name, t, dtype, shape):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+
+
+def shp_grouped_matmul(X, offsets, W, w_trans=False, out=None, dtype=torch.bfloat16):
+    """Y[t] = X[t] W[e] (or X[t] W[e]^T with w_trans) for the rows t in
+    offsets[e] .. offsets[e+1]-1 of each group e: the forward product of an
+    expert layer, or the gradient of its input.
+
+    X: [T, K] bf16, rows sorted by group; offsets: [groups + 1] int64 on the
+    device; W: [groups, K, N] bf16 ([groups, N, K] with w_trans).  Y: `out`, or
+    a new [T, N] tensor of `dtype` (bf16 or float32) whose rows outside every
+    group are uninitialised; in `out` those rows are left as they were."""
+    _dev(X, offsets, W, out)
+    _on_current(X, offsets, W, out)
+    if X.dim() != 2 or W.dim() != 3 or offsets.dim() != 1:
+        raise ValueError("X is [T, K], W [groups, K, N] and offsets [groups + 1]")
+    T, K = X.shape
+    groups, N = W.shape[0], W.shape[1] if w_trans else W.shape[2]
+    _want("X", X, torch.bfloat16, (T, K))
+    _want("W", W, torch.bfloat16, (groups, N, K) if w_trans else (groups, K, N))
+    _want("offsets", offsets, torch.int64, (groups + 1,))
+    out = torch.empty(T, N, dtype=dtype, device=X.device) if out is None else out
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("the result is bfloat16 or float32")
+    _want("out", out, out.dtype, (T, N))
+    storage = A.SHP_BF16 if out.dtype == torch.bfloat16 else A.SHP_TF32
+    _check(A.lib().shp_grouped_matmul(_p(X), _p(offsets), _p(W), int(bool(w_trans)), _p(out),
+                                      storage, T, K, N, groups, _stream()), "shp_grouped_matmul")
+    return out
+
+
+def shp_grouped_wgrad(Amat, B, offsets, out=None, accumulate=False):
+    """G[e] = A_e^T B_e over the rows of each group: the gradient of an expert
+    layer's weight blocks, in the fp32 layout shampoo_gram_ema takes.
+
+    A: [T, m], B: [T, n] bf16; offsets as in shp_grouped_matmul; G: `out`, or a
+    new [groups, m, n] float32 tensor.  accumulate adds to `out` (which must
+    then be given).  An empty group gives zeros, or leaves `out` as it is."""
+    _dev(Amat, B, offsets, out)
+    _on_current(Amat, B, offsets, out)
+    if Amat.dim() != 2 or B.dim() != 2 or offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError("A is [T, m], B [T, n] and offsets [groups + 1]")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    T, m = Amat.shape
+    n, groups = B.shape[1], offsets.shape[0] - 1
+    _want("A", Amat, torch.bfloat16, (T, m))
+    _want("B", B, torch.bfloat16, (T, n))
+    _want("offsets", offsets, torch.int64, (groups + 1,))
+    out = torch.empty(groups, m, n, dtype=torch.float32, device=B.device) if out is None else out
+    _want("out", out, torch.float32, (groups, m, n))
+    _check(A.lib().shp_grouped_wgrad(_p(Amat), _p(B), _p(offsets), _p(out), T, m, n, groups,
+                                     int(bool(accumulate)), _stream()), "shp_grouped_wgrad")
+    return out
+
+
 def shp_matmul_f64(Amat, B, out=None, ws=None, reuse_a=False, reuse_b=False, accumulate=False):
     """Batched C = A B in fp64-grade arithmetic on the int8 tensor cores (the
     Ozaki scheme); A [batch][M][K], B [batch][K][N] float64.  reuse_a /
