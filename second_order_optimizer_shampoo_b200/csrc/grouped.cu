@@ -45,7 +45,7 @@ constexpr int CHUNK_KB = 8;  // stages per fp32 chunk: sums of 512 products insi
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 32 * (2 + EPI_WARPS + 1);
 constexpr int EPI_BOX = 4096;  // one warp's 32-row store box
-constexpr int GSMEM = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * EPI_BOX + 256;
+constexpr int GSMEM = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * EPI_BOX + 320;
 static_assert(GSMEM <= 232448, "grouped kernel exceeds shared memory");
 
 // Byte offset of 16-byte group g of row r in a box of 128-byte rows stored
@@ -204,16 +204,18 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* accf = empty + STAGES;
   uint64_t* acce = accf + 2;
   uint64_t* tailb = acce + 2;        // per stage: a partial stage of this CTA has landed
-  uint64_t* drain = tailb + STAGES;  // all MMAs of this pair complete
+  uint64_t* clearb = tailb + STAGES;  // per stage (leader): the peer's half is cleared
+  uint64_t* drain = clearb + STAGES;  // all MMAs of this pair complete
   volatile int* abort_flag = reinterpret_cast<volatile int*>(drain + 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1) + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full[s], 2);  // one arrival per CTA
+      mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
       mbar_init(&tailb[s], 1);
+      mbar_init(&clearb[s], 1);
     }
     for (int u = 0; u < 2; ++u) {
       mbar_init(&accf[u], 1);
@@ -264,10 +266,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             continue;
           }
           const uint32_t fbar = mapa_shared(smem_u32(&full[s]), 0);
-          if (leader)
-            mbar_arrive_expect_tx(&full[s], 2 * STAGE_BYTES);
-          else
-            mbar_arrive_cluster(fbar);
+          if (leader) mbar_arrive_expect_tx(&full[s], 2 * STAGE_BYTES);
           if (A_MN) {
             for (int i = 0; i < 2; ++i)
               tma_load_3d_pair(sa + i * BK * 128, &tA, fbar, m0 + i * 64, k0, 0);
@@ -467,13 +466,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else if (WG) {
     // ---------------- clearing warp: rows behind the group in its last stage
     int kit = 0;
-    uint32_t par = 0;  // phase of each stage's tailb
+    uint32_t par = 0;  // phase of each stage's tailb and clearb
     while (walk.next(x)) {
       kit += x.kb;
       if (x.tail == 0) continue;
       const int s = (kit - 1) % STAGES;
       if (!warp_wait(&tailb[s], (par >> s) & 1, abort_flag)) break;
-      par ^= 1u << s;
       uint8_t* st = smem + s * STAGE_BYTES;
       const int r1 = (x.tail + 15) / 16 * 16;
       // four 64-column chunks (two of A, two of B) of 64 rows of 128 bytes
@@ -485,7 +483,15 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&full[s]), 0));
+      // the leader hands the stage over once both halves are cleared
+      if (!leader) {
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&clearb[s]), 0));
+      } else {
+        if (!warp_wait(&clearb[s], (par >> s) & 1, abort_flag)) break;
+        fence_cluster();
+        if (lane == 0) mbar_arrive(&full[s]);
+      }
+      par ^= 1u << s;
     }
   }
 
