@@ -62,7 +62,7 @@ typedef enum {
 typedef enum {
   SHP_TF32 = 0,   /* fp32 storage, products on TF32 tensor cores                  */
   SHP_3XTF32 = 1, /* fp32 storage split as hi (TF32) + lo; acc += hh + hl + lh     */
-  SHP_BF16 = 2,   /* bf16 storage, fp32 accumulation (polar factor only)           */
+  SHP_BF16 = 2,   /* bf16 storage, fp32 accumulation (polar factor, plain products) */
   SHP_OZAKI = 3   /* fp64 storage; every product split into five int8 digit slices
                      per operand and accumulated exactly on the int8 tensor cores
                      (about 2^-40 of the row/column maxima per product; inverse
@@ -345,6 +345,48 @@ int shp_grouped_matmul(const void* X, const int64_t* offsets, const void* W, int
  * group's G is set to zero, or left as it is when accumulating. */
 int shp_grouped_wgrad(const void* A, const void* B, const int64_t* offsets, float* G, int64_t T,
                       int64_t m, int64_t n, int64_t groups, int accumulate, shp_stream stream);
+
+/* ---- Microscaled 4-bit floating point (no counterpart on the pages). ----
+ *
+ * MXFP4 of the OCP Microscaling Formats specification v1.0: a block of 32
+ * values x shares the scale 2^e, e = floor(log2 max|x|) - 2 (at least -127),
+ * stored as the byte e + 127; a value is a sign and one of 0, 0.5, 1, 1.5, 2,
+ * 3, 4, 6 (codes 0..7, sign in bit 3): x / 2^e rounded to nearest, ties to the
+ * even code, saturated at 6.  A block of zeros has scale byte 0; a block that
+ * holds a NaN or an Inf has scale byte 255 (NaN) and zero codes, so it reads
+ * back, and multiplies, as NaN.
+ *
+ * Layout of a quantised [batch][rows][cols] matrix, blocks along the columns:
+ *   codes   [batch][rows][Cp / 2] bytes, Cp = cols rounded up to 32: column 2j
+ *           in the low nibble of byte j, zero codes behind cols
+ *   scales  [batch][ceil(rows / 128)][ceil(cols / 128)] tiles of 512 bytes (128
+ *           rows x 4 blocks): row r and block k of a tile at byte
+ *           (r % 32) * 16 + (r / 32) * 4 + k; scale byte 0 for rows and blocks
+ *           outside the matrix (a product multiplies the scales of a partial
+ *           tile's last block pair by zero codes: they must not be 255)
+ * All four buffers 16-byte aligned. */
+size_t shp_mx4_code_bytes(int64_t rows, int64_t cols, int64_t batch);
+size_t shp_mx4_scale_bytes(int64_t rows, int64_t cols, int64_t batch);
+
+/* Quantises X: [batch][rows][cols], fp32 (storage = SHP_TF32) or bf16
+ * (SHP_BF16), from one read of it: blocks along the columns into Q, S, and /
+ * or blocks along the rows into Qt, St, which are the codes and scales of X^T
+ * ([batch][cols][rows]: the operand of a product that contracts over rows,
+ * such as the gradient of a quantised product).  Either pair may be NULL. */
+int shp_mx4_quantize(const void* X, int storage, int64_t rows, int64_t cols, int64_t batch,
+                     void* Q, void* S, void* Qt, void* St, shp_stream stream);
+
+/* The values of a quantised matrix, exact in fp32 and in bf16; any cols. */
+int shp_mx4_dequantize(const void* Q, const void* S, int64_t rows, int64_t cols, int64_t batch,
+                       void* X, int storage, shp_stream stream);
+
+/* C[b] = A[b] B[b]^T on the 4-bit tensor cores, sums in fp32.  A: [batch][M][K]
+ * and B: [batch][N][K], both quantised along K (a multiple of 32: Cp above);
+ * C: [batch][M][N], bf16 (SHP_BF16, N a multiple of 8) or fp32 (SHP_TF32, N a
+ * multiple of 4).  batch <= 65535.  No workspace. */
+int shp_mx4_matmul(const void* A, const void* A_scales, const void* B, const void* B_scales,
+                   void* C, int out_storage, int64_t M, int64_t N, int64_t K, int64_t batch,
+                   shp_stream stream);
 
 /* Number of kernels this library has launched in the process so far
  * (host-side counter, all threads and devices). */

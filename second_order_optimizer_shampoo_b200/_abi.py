@@ -35,6 +35,8 @@ EXPORTS = ("shp_workspace_bytes", "shampoo_gram_ema", "shampoo_gram_ema_steps", 
            "matfn_sign",
            "prism_alpha_fit", "shampoo_apply", "shampoo_apply_ex", "shp_matmul", "shp_split_tf32",
            "shp_grouped_matmul", "shp_grouped_wgrad",
+           "shp_mx4_code_bytes", "shp_mx4_scale_bytes", "shp_mx4_quantize", "shp_mx4_dequantize",
+           "shp_mx4_matmul",
            "shp_matmul_f64_workspace_bytes", "shp_matmul_f64", "shp_matmul_f64_ex",
            "shp_kernel_launches", "prism_alpha_fit_noalloc", "shp_selftest_bounded_wait", "shp_status_string", "shp_last_cuda_error",
            "shp_version")
@@ -84,6 +86,11 @@ _SIGS = {
     "shp_split_tf32": (_INT, [_P, _I64, _P, _P, _P]),
     "shp_grouped_matmul": (_INT, [_P, _P, _P, _INT, _P, _INT, _I64, _I64, _I64, _I64, _P]),
     "shp_grouped_wgrad": (_INT, [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _INT, _P]),
+    "shp_mx4_code_bytes": (_SZ, [_I64, _I64, _I64]),
+    "shp_mx4_scale_bytes": (_SZ, [_I64, _I64, _I64]),
+    "shp_mx4_quantize": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _P, _P, _P, _P]),
+    "shp_mx4_dequantize": (_INT, [_P, _P, _I64, _I64, _I64, _P, _INT, _P]),
+    "shp_mx4_matmul": (_INT, [_P, _P, _P, _P, _P, _INT, _I64, _I64, _I64, _I64, _P]),
     "shp_matmul_f64_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64]),
     "shp_matmul_f64": (_INT, [_P, _P, _P, _I64, _I64, _I64, _I64, _P, _SZ, _P]),
     "shp_matmul_f64_ex": (_INT, [_P, _P, _P, _I64, _I64, _I64, _I64, _INT, _P, _SZ, _P]),

@@ -452,7 +452,8 @@ const char* shp_version(void) { return "0.1.0"; }
 uint64_t shp_kernel_launches(void) {
   if (cudaDeviceSynchronize() != cudaSuccess) return 0;
   return kernel_runs_gemm() + kernel_runs_sketch() + kernel_runs_elementwise() +
-         kernel_runs_small() + kernel_runs_ozaki() + kernel_runs_grouped();
+         kernel_runs_small() + kernel_runs_ozaki() + kernel_runs_grouped() +
+         kernel_runs_mx4();
 }
 
 int shp_split_tf32(const float* X, int64_t count, float* hi, float* lo, shp_stream stream) {
@@ -511,6 +512,64 @@ int shp_grouped_wgrad(const void* A, const void* B, const int64_t* offsets, floa
   CK(grouped_wgrad(A, B, offsets, G, static_cast<int>(T), static_cast<int>(m),
                    static_cast<int>(n), static_cast<int>(groups), accumulate != 0,
                    static_cast<cudaStream_t>(stream)));
+  return SHP_OK;
+}
+
+size_t shp_mx4_code_bytes(int64_t rows, int64_t cols, int64_t batch) {
+  if (rows <= 0 || cols <= 0 || batch <= 0 || rows > kMaxRows || cols > kMaxRows) return 0;
+  return static_cast<size_t>(batch) * rows * ((cols + 31) / 32) * 16;
+}
+
+size_t shp_mx4_scale_bytes(int64_t rows, int64_t cols, int64_t batch) {
+  if (rows <= 0 || cols <= 0 || batch <= 0 || rows > kMaxRows || cols > kMaxRows) return 0;
+  return static_cast<size_t>(batch) * ((rows + 127) / 128) * ((cols + 127) / 128) * 512;
+}
+
+int shp_mx4_quantize(const void* X, int storage, int64_t rows, int64_t cols, int64_t batch,
+                     void* Q, void* S, void* Qt, void* St, shp_stream stream) {
+  if (!X || rows <= 0 || cols <= 0 || batch <= 0) return SHP_EINVAL;
+  if (storage != SHP_BF16 && storage != SHP_TF32) return SHP_EINVAL;
+  if ((Q == nullptr) != (S == nullptr) || (Qt == nullptr) != (St == nullptr) || (!Q && !Qt))
+    return SHP_EINVAL;
+  if (cols % (storage == SHP_BF16 ? 8 : 4)) return SHP_EINVAL;
+  if (!aligned16(X) || !aligned16(Q) || !aligned16(S) || !aligned16(Qt) || !aligned16(St))
+    return SHP_EINVAL;
+  if (rows > kMaxRows || cols > kMaxRows || batch > INT32_MAX) return SHP_EUNSUPPORTED;
+  if (batch * ((rows + 127) / 128) > INT32_MAX / ((cols + 127) / 128)) return SHP_EUNSUPPORTED;
+  CK(mx4_quantize(X, storage == SHP_BF16, static_cast<int>(rows), static_cast<int>(cols), batch,
+                  static_cast<uint8_t*>(Q), static_cast<uint8_t*>(S), static_cast<uint8_t*>(Qt),
+                  static_cast<uint8_t*>(St), static_cast<cudaStream_t>(stream)));
+  return SHP_OK;
+}
+
+int shp_mx4_dequantize(const void* Q, const void* S, int64_t rows, int64_t cols, int64_t batch,
+                       void* X, int storage, shp_stream stream) {
+  if (!Q || !S || !X || rows <= 0 || cols <= 0 || batch <= 0) return SHP_EINVAL;
+  if (storage != SHP_BF16 && storage != SHP_TF32) return SHP_EINVAL;
+  if (!aligned16(Q) || !aligned16(S) || !aligned16(X)) return SHP_EINVAL;
+  if (rows > kMaxRows || cols > kMaxRows || batch > INT32_MAX) return SHP_EUNSUPPORTED;
+  CK(mx4_dequantize(static_cast<const uint8_t*>(Q), static_cast<const uint8_t*>(S),
+                    static_cast<int>(rows), static_cast<int>(cols), batch, X,
+                    storage == SHP_BF16, static_cast<cudaStream_t>(stream)));
+  return SHP_OK;
+}
+
+int shp_mx4_matmul(const void* A, const void* A_scales, const void* B, const void* B_scales,
+                   void* C, int out_storage, int64_t M, int64_t N, int64_t K, int64_t batch,
+                   shp_stream stream) {
+  if (!A || !A_scales || !B || !B_scales || !C) return SHP_EINVAL;
+  if (M <= 0 || N <= 0 || K <= 0 || batch <= 0) return SHP_EINVAL;
+  if (out_storage != SHP_BF16 && out_storage != SHP_TF32) return SHP_EINVAL;
+  if (K % 32 || N % (out_storage == SHP_BF16 ? 8 : 4)) return SHP_EINVAL;
+  if (!aligned16(A) || !aligned16(A_scales) || !aligned16(B) || !aligned16(B_scales) ||
+      !aligned16(C))
+    return SHP_EINVAL;
+  if (M > kMaxRows || N > kMaxRows || K > kMaxRows || batch > 65535) return SHP_EUNSUPPORTED;
+  if (batch * ((M + 127) / 128) > INT32_MAX / 2 / ((N + 127) / 128)) return SHP_EUNSUPPORTED;
+  CK(mx4_gemm(static_cast<const uint8_t*>(A), static_cast<const uint8_t*>(A_scales),
+              static_cast<const uint8_t*>(B), static_cast<const uint8_t*>(B_scales), C,
+              out_storage == SHP_TF32, static_cast<int>(M), static_cast<int>(N),
+              static_cast<int>(K), batch, static_cast<cudaStream_t>(stream)));
   return SHP_OK;
 }
 

@@ -48,12 +48,6 @@ constexpr int EPI_BOX = 4096;  // one warp's 32-row store box
 constexpr int GSMEM = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * EPI_BOX + 320;
 static_assert(GSMEM <= 232448, "grouped kernel exceeds shared memory");
 
-// Byte offset of 16-byte group g of row r in a box of 128-byte rows stored
-// with the 128-byte swizzle.
-SHP_DEV uint32_t sw128_off(int r, int g) {
-  return static_cast<uint32_t>(r * 128 + ((g ^ (r & 7)) << 4));
-}
-
 SHP_DEV void tma_reduce_add_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
   asm volatile(
       "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group"
@@ -63,15 +57,6 @@ SHP_DEV void tma_reduce_add_3d(const CUtensorMap* map, const void* src, int x, i
 }
 
 SHP_DEV void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
-
-// A whole warp waits; false for every lane if one lane's wait gave up, so that
-// the warp leaves its loop together.
-SHP_DEV bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  const bool ok = *abort_flag == 0 && mbar_wait(bar, parity, abort_flag);
-  if (__all_sync(0xffffffffu, ok)) return true;
-  *abort_flag = 1;
-  return false;
-}
 
 // Group e covers the rows [lo, hi): the offsets clamped to 0..T and to
 // non-negative lengths, so that no offset array reaches outside the operands.

@@ -382,5 +382,17 @@ cudaError_t grouped_wgrad(const void* A, const void* B, const int64_t* offsets, 
                           int M, int N, int groups, bool accumulate, cudaStream_t st);
 uint64_t kernel_runs_grouped();
 
+// ---- Microscaled 4-bit floating point (mx4.cu; layouts in the public header)
+// Codes and scale tiles of X ([batch][rows][cols], fp32 or bf16) in blocks
+// along the columns (Q, S) and / or of X^T in blocks along the rows (Qt, St).
+cudaError_t mx4_quantize(const void* X, bool bf16, int rows, int cols, int64_t batch, uint8_t* Q,
+                         uint8_t* S, uint8_t* Qt, uint8_t* St, cudaStream_t st);
+cudaError_t mx4_dequantize(const uint8_t* Q, const uint8_t* S, int rows, int cols, int64_t batch,
+                           void* X, bool bf16, cudaStream_t st);
+// C[b] (M x N) = A[b] (M x K) B[b]^T (N x K), K a multiple of 32.
+cudaError_t mx4_gemm(const uint8_t* A, const uint8_t* As, const uint8_t* B, const uint8_t* Bs,
+                     void* C, bool f32, int M, int N, int K, int64_t batch, cudaStream_t st);
+uint64_t kernel_runs_mx4();
+
 
 }  // namespace shp

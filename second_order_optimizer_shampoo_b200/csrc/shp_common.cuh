@@ -76,6 +76,15 @@ SHP_DEV void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// A whole warp waits; false for every lane if one lane's wait gave up, so that
+// the warp leaves its loop together.
+SHP_DEV bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  const bool ok = *abort_flag == 0 && mbar_wait(bar, parity, abort_flag);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  *abort_flag = 1;
+  return false;
+}
+
 // ----------------------------------------------------------------- TMA
 SHP_DEV void tma_prefetch_desc(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
@@ -89,6 +98,12 @@ SHP_DEV void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
+}
+
+// Byte offset of 16-byte group g of row r in a box of 128-byte rows stored
+// with the 128-byte swizzle.
+SHP_DEV uint32_t sw128_off(int r, int g) {
+  return static_cast<uint32_t>(r * 128 + ((g ^ (r & 7)) << 4));
 }
 
 // 3-D tiled bulk-tensor store shared -> global of the box at {x, y, z}, in

@@ -333,12 +333,9 @@ def shp_grouped_matmul(X, offsets, W, w_trans=False, out=None, dtype=torch.bfloa
     _want("W", W, torch.bfloat16, (groups, N, K) if w_trans else (groups, K, N))
     _want("offsets", offsets, torch.int64, (groups + 1,))
     out = torch.empty(T, N, dtype=dtype, device=X.device) if out is None else out
-    if out.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError("the result is bfloat16 or float32")
     _want("out", out, out.dtype, (T, N))
-    storage = A.SHP_BF16 if out.dtype == torch.bfloat16 else A.SHP_TF32
     _check(A.lib().shp_grouped_matmul(_p(X), _p(offsets), _p(W), int(bool(w_trans)), _p(out),
-                                      storage, T, K, N, groups, _stream()), "shp_grouped_matmul")
+                                      _storage(out.dtype), T, K, N, groups, _stream()), "shp_grouped_matmul")
     return out
 
 
@@ -364,6 +361,78 @@ def shp_grouped_wgrad(Amat, B, offsets, out=None, accumulate=False):
     _want("out", out, torch.float32, (groups, m, n))
     _check(A.lib().shp_grouped_wgrad(_p(Amat), _p(B), _p(offsets), _p(out), T, m, n, groups,
                                      int(bool(accumulate)), _stream()), "shp_grouped_wgrad")
+    return out
+
+
+_STORAGE = {torch.bfloat16: A.SHP_BF16, torch.float32: A.SHP_TF32}
+
+
+def _storage(dtype):
+    if dtype not in _STORAGE:
+        raise ValueError(f"bfloat16 or float32, not {dtype}")
+    return _STORAGE[dtype]
+
+
+def _mx4_shapes(batch, rows, cols):
+    return ((batch, rows, (cols + 31) // 32 * 16),
+            (batch, (rows + 127) // 128, (cols + 127) // 128, 512))
+
+
+def shp_mx4_quantize(X, along="cols"):
+    """MXFP4 codes and scales of X ([batch, rows, cols] or [rows, cols], bf16 or
+    float32), in blocks of 32 along the columns: (Q, S); along="rows" gives
+    those of X^T, blocks along X's rows: (Qt, St); along="both" gives (Q, S,
+    Qt, St) from one read of X.  Q: uint8 [batch, rows, Cp / 2], S: uint8
+    [batch, rows / 128, cols / 128, 512] tiles (rounded up); layouts in the C
+    header."""
+    _dev(X)
+    _on_current(X)
+    if along not in ("cols", "rows", "both") or X.dim() not in (2, 3):
+        raise ValueError("X is [batch, rows, cols] or [rows, cols]; along is cols, rows or both")
+    rows, cols = X.shape[-2], X.shape[-1]
+    batch = X.shape[0] if X.dim() == 3 else 1
+    new = lambda shapes: [torch.empty(s, dtype=torch.uint8, device=X.device) for s in shapes]  # noqa: E731
+    q = new(_mx4_shapes(batch, rows, cols)) if along != "rows" else [None, None]
+    qt = new(_mx4_shapes(batch, cols, rows)) if along != "cols" else [None, None]
+    _check(A.lib().shp_mx4_quantize(_p(X), _storage(X.dtype), rows, cols, batch, _p(q[0]), _p(q[1]),
+                                    _p(qt[0]), _p(qt[1]), _stream()), "shp_mx4_quantize")
+    return tuple(t for t in q + qt if t is not None)
+
+
+def shp_mx4_dequantize(Q, S, cols, dtype=torch.float32, out=None):
+    """The values [batch, rows, cols] of MXFP4 codes and scales."""
+    _dev(Q, S, out)
+    _on_current(Q, S, out)
+    if Q.dim() != 3:
+        raise ValueError("Q is [batch, rows, Cp / 2]")
+    batch, rows = Q.shape[0], Q.shape[1]
+    for name, t, shape in zip(("Q", "S"), (Q, S), _mx4_shapes(batch, rows, cols)):
+        _want(name, t, torch.uint8, shape)
+    out = torch.empty(batch, rows, cols, dtype=dtype, device=Q.device) if out is None else out
+    _want("out", out, out.dtype, (batch, rows, cols))
+    _check(A.lib().shp_mx4_dequantize(_p(Q), _p(S), rows, cols, batch, _p(out),
+                                      _storage(out.dtype), _stream()), "shp_mx4_dequantize")
+    return out
+
+
+def shp_mx4_matmul(Amat, A_scales, B, B_scales, dtype=torch.bfloat16, out=None):
+    """C[b] = A[b] B[b]^T of two MXFP4 operands quantised along the contraction:
+    A [batch, M, K / 2] and B [batch, N, K / 2] with their scale tiles.  C:
+    `out`, or a new [batch, M, N] tensor of `dtype` (bf16 or float32)."""
+    _dev(Amat, A_scales, B, B_scales, out)
+    _on_current(Amat, A_scales, B, B_scales, out)
+    if Amat.dim() != 3 or B.dim() != 3:
+        raise ValueError("A is [batch, M, K / 2] and B [batch, N, K / 2]")
+    batch, M, K = Amat.shape[0], Amat.shape[1], Amat.shape[2] * 2
+    N = B.shape[1]
+    for name, t, shape in zip(("A", "A_scales", "B", "B_scales"), (Amat, A_scales, B, B_scales),
+                              _mx4_shapes(batch, M, K) + _mx4_shapes(batch, N, K)):
+        _want(name, t, torch.uint8, shape)
+    out = torch.empty(batch, M, N, dtype=dtype, device=B.device) if out is None else out
+    _want("out", out, out.dtype, (batch, M, N))
+    _check(A.lib().shp_mx4_matmul(_p(Amat), _p(A_scales), _p(B), _p(B_scales), _p(out),
+                                  _storage(out.dtype), M, N, K, batch, _stream()),
+           "shp_mx4_matmul")
     return out
 
 
