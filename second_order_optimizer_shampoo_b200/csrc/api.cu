@@ -548,6 +548,7 @@ int shp_mx4_dequantize(const void* Q, const void* S, int64_t rows, int64_t cols,
   if (storage != SHP_BF16 && storage != SHP_TF32) return SHP_EINVAL;
   if (!aligned16(Q) || !aligned16(S) || !aligned16(X)) return SHP_EINVAL;
   if (rows > kMaxRows || cols > kMaxRows || batch > INT32_MAX) return SHP_EUNSUPPORTED;
+  if (batch * ((rows + 127) / 128) > INT32_MAX / ((cols + 127) / 128)) return SHP_EUNSUPPORTED;
   CK(mx4_dequantize(static_cast<const uint8_t*>(Q), static_cast<const uint8_t*>(S),
                     static_cast<int>(rows), static_cast<int>(cols), batch, X,
                     storage == SHP_BF16, static_cast<cudaStream_t>(stream)));

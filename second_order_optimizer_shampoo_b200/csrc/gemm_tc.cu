@@ -1238,6 +1238,26 @@ bool tensor_map_rows(CUtensorMap* m, const float* ptr, int64_t inner, int64_t ro
                   CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+LaunchInfo launch_info(const void* kernel, int smem, std::atomic<uint64_t>& done) {
+  static std::atomic<int> sms[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return {e, 0};
+  int n = dev < 64 ? sms[dev].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return {e, 0};
+    if (dev < 64) sms[dev].store(n, std::memory_order_relaxed);
+  }
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if ((done.load(std::memory_order_acquire) & bit) == 0) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return {e, 0};
+    done.fetch_or(bit, std::memory_order_release);
+  }
+  return {cudaSuccess, n};
+}
+
 bool tensor_map(CUtensorMap* m, const void* ptr, int esz, int64_t inner, int64_t rows,
                 int64_t batch, int64_t ld, int64_t bstride, int box_inner, int box_rows,
                 CUtensorMapSwizzle swz) {

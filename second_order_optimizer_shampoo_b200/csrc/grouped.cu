@@ -491,12 +491,10 @@ template <bool WG, bool B_MN, bool F32>
 cudaError_t launch_grouped(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
                            const GroupedParams& p, int64_t max_tiles, cudaStream_t st) {
   auto kern = k_grouped<WG, B_MN, F32>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GSMEM);
-  if (e != cudaSuccess) return e;
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess)
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  int64_t ncl = sms / 2;
+  static std::atomic<uint64_t> done{0};
+  const LaunchInfo li = launch_info(reinterpret_cast<const void*>(kern), GSMEM, done);
+  if (li.err != cudaSuccess) return li.err;
+  int64_t ncl = li.sms / 2;
   if (ncl > max_tiles) ncl = max_tiles;
   if (ncl < 1) ncl = 1;
   cudaLaunchConfig_t cfg = {};

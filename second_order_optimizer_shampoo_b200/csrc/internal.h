@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "shampoo_prism.h"
 
 namespace shp {
@@ -371,6 +373,15 @@ cudaError_t oz_gform_d1(const double* R, int64_t n, int batch, const Ctl& ctl, d
 cudaError_t oz_finish(int64_t n, int batch, const Ctl& ctl, double c_exponent, const double* S,
                       float* X_out, bool z_slots, cudaStream_t st);
 uint64_t kernel_runs_ozaki();
+
+// Launch state of a kernel that is set once per device: the opt-in to `smem`
+// bytes of dynamic shared memory (`done`: one bit per device, owned by the
+// caller, one per kernel), and the device's SM count.
+struct LaunchInfo {
+  cudaError_t err;
+  int sms;
+};
+LaunchInfo launch_info(const void* kernel, int smem, std::atomic<uint64_t>& done);
 
 // ---- Products of rows grouped by expert (grouped.cu); bf16 operands
 // Y[t] = X[t] W_e (W: [groups][K][N]) or X[t] W_e^T (w_trans, W: [groups][N][K])

@@ -15,6 +15,7 @@
 // tcgen05.cp.32x128b brings a tile's scales into tensor memory.  Scales of
 // rows and blocks outside the matrix are zero bytes.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <string.h>
 
 #include "internal.h"
@@ -26,9 +27,7 @@ namespace {
 
 // ------------------------------------------------------------ quantisation
 
-constexpr int QT = 128;       // rows and columns of a quantiser tile
-constexpr int QLD = QT + 4;   // floats per tile row in shared memory (see k_mx4_quantize)
-constexpr int QSMEM = QT * QLD * 4;
+constexpr int QT = 128;  // rows and columns of a quantiser tile
 
 // Codes of eight values, the first in the lowest nibble.
 SHP_DEV uint32_t e2m1x8(const float* y) {
@@ -67,157 +66,252 @@ SHP_DEV uint32_t quantize_block(float* x, uint32_t* q) {
   return static_cast<uint32_t>(sb);
 }
 
-// One orientation's outputs: codes of `lines` lines (rows, or columns of X)
-// of `len` values, and their scale tiles.
-struct Mx4Out {
-  uint8_t* q;
-  uint8_t* s;
+// k_mx4_quantize reads X once, in 128 x 128 tiles, along either axis or both.
+// It moves bytes and computes little, so one persistent CTA per SM keeps
+// several tiles in flight: warp 16 brings them by TMA (zero fill outside X)
+// into a ring, 16 warps quantise, a block of 32 values per thread and
+// orientation, and the codes and the 512 scale bytes of a tile leave as bulk
+// stores (which clip the edge).  The tile stays in X's type, in boxes of
+// 128-byte rows with the 128-byte swizzle: a warp whose lanes own 32 rows
+// (16-byte reads) and one whose lanes own 32 columns both read it without bank
+// conflicts, so one copy serves both orientations.
+constexpr int QTHREADS = 512;
+constexpr int QSTG = 2 * 8192 + 2 * 512;  // codes and scales of both orientations
+
+template <bool BF16>
+struct QCfg {
+  static constexpr int TILE = QT * QT * (BF16 ? 2 : 4);
+  static constexpr int STAGES = BF16 ? 5 : 3;
+  static constexpr int SMEM = 1024 + STAGES * TILE + QSTG + 128;
 };
 
-// A CTA quantises one 128 x 128 tile of X, read once (16-byte loads, a warp
-// per row), along either axis or both.  The tile is kept as fp32 in shared
-// memory with rows of 132 floats: threads that own a row read it 16 bytes at
-// a time and threads that own a column 4 bytes at a time, both without bank
-// conflicts.  A thread quantises two neighbouring blocks of a line, so its
-// codes are 32 contiguous bytes, and the tile's scales leave as one 512-byte
-// run.
+struct QParams {
+  int rows, cols, tiles_r, tiles_c;
+  int64_t tiles;
+  uint8_t* s[2];  // scale tiles per orientation (null: not wanted)
+};
+
+SHP_DEV void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+               "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+SHP_DEV void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(QTHREADS) : "memory"); }
+
 template <bool BF16>
-__global__ void __launch_bounds__(256)
-    k_mx4_quantize(const void* X, int rows, int cols, int tiles_r, int tiles_c, Mx4Out orow,
-                   Mx4Out ocol) {
+__global__ void __launch_bounds__(QTHREADS + 32, 1)
+    k_mx4_quantize(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CUtensorMap tQ,
+                   const __grid_constant__ CUtensorMap tQt, QParams p) {
   count_kernel_run();
-  extern __shared__ __align__(16) float xs[];
-  __shared__ uint32_t sc[2][128];
-  const int64_t t = blockIdx.x;
-  const int tc = static_cast<int>(t % tiles_c);
-  const int tr = static_cast<int>(t / tiles_c % tiles_r);
-  const int64_t b = t / tiles_c / tiles_r;
-  const int r0 = tr * QT, c0 = tc * QT;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t base = b * rows * static_cast<int64_t>(cols) + c0 + 4 * lane;
-  const bool cin = c0 + 4 * lane < cols;  // cols is a multiple of 4
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    float4 v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = r0 + warp + 8 * (8 * half + i);
-      v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (cin && r < rows) {
-        const int64_t at = base + r * static_cast<int64_t>(cols);
-        if (BF16) {
-          const uint2 u = __ldg(reinterpret_cast<const uint2*>(
-              static_cast<const __nv_bfloat16*>(X) + at));
-          v[i] = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-                             __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
-        } else {
-          v[i] = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(X) + at));
-        }
-      }
+  using C = QCfg<BF16>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* stg = smem + C::STAGES * C::TILE;
+  uint64_t* full = reinterpret_cast<uint64_t*>(stg + QSTG);
+  uint64_t* empty = full + C::STAGES;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + C::STAGES);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], QTHREADS / 32);
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      *reinterpret_cast<float4*>(xs + (warp + 8 * (8 * half + i)) * QLD + 4 * lane) = v[i];
+    *abort_flag = 0;
+    fence_barrier_init();
   }
   __syncthreads();
-  const int line = threadIdx.x & 127, h = threadIdx.x >> 7;  // blocks 2h, 2h + 1 of a line
-#pragma unroll 1
-  for (int o = 0; o < 2; ++o) {
-    const Mx4Out out = o == 0 ? orow : ocol;
-    if (out.q == nullptr) continue;
-    const int lines = o == 0 ? rows : cols, len = o == 0 ? cols : rows;
-    const int l0 = o == 0 ? r0 : c0, p0 = o == 0 ? c0 : r0;
-    const int blocks = (len + 31) / 32;
-    const int tl = o == 0 ? tr : tc, tp = o == 0 ? tc : tr;
-    const int tiles_l = o == 0 ? tiles_r : tiles_c, tiles_p = o == 0 ? tiles_c : tiles_r;
-    uint32_t bytes = 0;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t per_b = static_cast<int64_t>(p.tiles_r) * p.tiles_c;
+  if (warp == QTHREADS / 32) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tX);
+      int it = 0;
+      for (int64_t t = blockIdx.x; t < p.tiles; t += gridDim.x, ++it) {
+        const int s = it % C::STAGES;
+        if (it >= C::STAGES && !mbar_wait(&empty[s], ((it / C::STAGES) - 1) & 1)) {
+          // the consumers gave up: let the copies in flight land (bounded)
+          for (int i = it - C::STAGES; i < it; ++i)
+            mbar_wait(&full[i % C::STAGES], (i / C::STAGES) & 1);
+          break;
+        }
+        const int b = static_cast<int>(t / per_b), r = static_cast<int>(t % per_b);
+        const int c0 = r % p.tiles_c * QT, r0 = r / p.tiles_c * QT;
+        mbar_arrive_expect_tx(&full[s], C::TILE);
+        constexpr int W = BF16 ? 64 : 32;  // columns per box
+        for (int i = 0; i < QT / W; ++i)
+          tma_load_3d(smem + s * C::TILE + i * QT * 128, &tX, &full[s], c0 + i * W, r0, b);
+      }
+    }
+    return;
+  }
+  const int line = threadIdx.x & 127, k = threadIdx.x >> 7;  // block k of a row, or column, `line`
+  int it = 0;
+  for (int64_t t = blockIdx.x; t < p.tiles; t += gridDim.x, ++it) {
+    const int s = it % C::STAGES;
+    const uint8_t* tile = smem + s * C::TILE;
+    // a wait that gives up is acted on behind the barrier below, by all warps
+    // together (only consumers set the flag)
+    if (!mbar_wait(&full[s], (it / C::STAGES) & 1)) *abort_flag = 1;
+    uint32_t q[2][4], sb[2];
+    if (p.s[0] != nullptr) {
       float x[32];
-      const int p = 64 * h + 32 * k;
-      if (o == 0) {
+      if (BF16) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 v = *reinterpret_cast<const float4*>(xs + line * QLD + p + 4 * i);
-          x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+        for (int i = 0; i < 4; ++i) {
+          const uint4 u = *reinterpret_cast<const uint4*>(
+              tile + (k >> 1) * QT * 128 + sw128_off(line, (k & 1) * 4 + i));
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+            x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+          }
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = xs[(p + i) * QLD + line];
+        for (int i = 0; i < 8; ++i) {
+          const float4 v =
+              *reinterpret_cast<const float4*>(tile + k * QT * 128 + sw128_off(line, i));
+          x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+        }
       }
-      uint32_t q[4];
-      bytes |= quantize_block(x, q) << (8 * k);
-      if (l0 + line < lines && (p0 + p) / 32 < blocks)
-        *reinterpret_cast<uint4*>(out.q + ((b * lines + l0 + line) * blocks + (p0 + p) / 32) * 16) =
-            make_uint4(q[0], q[1], q[2], q[3]);
+      sb[0] = quantize_block(x, q[0]);
     }
-    // word (r % 32) * 4 + r / 32 of the tile holds a line's four scale bytes
-    if (h == 1) sc[0][(line & 31) * 4 + (line >> 5)] = bytes << 16;
-    __syncthreads();
-    if (h == 0) sc[1][(line & 31) * 4 + (line >> 5)] = sc[0][(line & 31) * 4 + (line >> 5)] | bytes;
-    __syncthreads();
-    if (h == 0)
-      reinterpret_cast<uint32_t*>(out.s)[((b * tiles_l + tl) * tiles_p + tp) * 128 + line] =
-          sc[1][line];
-    __syncthreads();
+    if (p.s[1] != nullptr) {
+      float x[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const int r = 32 * k + i;  // r & 7 == i & 7
+        if (BF16)
+          x[i] = __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(
+                     tile + (line >> 6) * QT * 128 + sw128_off(r, (line & 63) >> 3) +
+                     (line & 7) * 2)) << 16);
+        else
+          x[i] = *reinterpret_cast<const float*>(tile + (line >> 5) * QT * 128 +
+                                                 sw128_off(r, (line & 31) >> 2) + (line & 3) * 4);
+      }
+      sb[1] = quantize_block(x, q[1]);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[s]);
+    if (threadIdx.x == 0) bulk_wait_read_all();  // the last tile's stores have read the staging
+    consumers_sync();
+    if (*abort_flag) break;
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+      if (p.s[o] == nullptr) continue;
+      *reinterpret_cast<uint4*>(stg + o * 8192 + line * 64 + ((k ^ ((line >> 1) & 3)) << 4)) =
+          make_uint4(q[o][0], q[o][1], q[o][2], q[o][3]);
+      stg[2 * 8192 + o * 512 + (line & 31) * 16 + (line >> 5) * 4 + k] =
+          static_cast<uint8_t>(sb[o]);
+    }
+    fence_proxy_async_smem();
+    consumers_sync();
+    if (threadIdx.x == 0) {
+      const int b = static_cast<int>(t / per_b), r = static_cast<int>(t % per_b);
+      const int tc = r % p.tiles_c, tr = r / p.tiles_c;
+      if (p.s[0] != nullptr) {
+        tma_store_3d(&tQ, stg, tc * 32, tr * QT, b);
+        bulk_store(p.s[0] + t * 512, stg + 2 * 8192, 512);
+      }
+      if (p.s[1] != nullptr) {
+        tma_store_3d(&tQt, stg + 8192, tr * 32, tc * QT, b);
+        bulk_store(p.s[1] + (b * per_b + static_cast<int64_t>(tc) * p.tiles_r + tr) * 512,
+                   stg + 2 * 8192 + 512, 512);
+      }
+      bulk_commit();
+    }
   }
+  if (threadIdx.x == 0) bulk_wait_all();
 }
 
-// Eight values per thread: a coalesced 4-byte read of codes, 16 or 32 bytes
-// written.  Values are exact in either type (one mantissa bit, and exponents
-// down to 2^-128).
+// Two codes (one byte of `w`) as fp32.
+SHP_DEV void e2m1x2(uint32_t w, float& a, float& b) {
+  uint32_t h;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t}"
+      : "=r"(h)
+      : "r"(w));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  a = f.x;
+  b = f.y;
+}
+
+// A CTA restores one 128 x 128 tile; a warp's store is one (fp32: 4 values per
+// lane) or two (bf16: 8 values per lane) contiguous row segments, and each
+// lane has eight loads of codes in flight.  Values are exact in either type
+// (one mantissa bit, exponents down to 2^-128).
 template <bool BF16>
 __global__ void __launch_bounds__(256)
-    k_mx4_dequantize(const uint8_t* Q, const uint8_t* S, int rows, int cols, int64_t batch,
-                     void* X) {
+    k_mx4_dequantize(const uint8_t* Q, const uint8_t* S, int rows, int cols, int tiles_r,
+                     int tiles_c, void* X) {
   count_kernel_run();
-  const int groups = (cols + 7) / 8, blocks = (cols + 31) / 32;
-  const int tiles_r = (rows + 127) / 128, tiles_c = (blocks + 3) / 4;
-  const int64_t n = batch * rows * groups;
-  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int g = static_cast<int>(i % groups);
-    const int64_t br = i / groups;
-    const int r = static_cast<int>(br % rows);
-    const int64_t b = br / rows;
-    const uint32_t codes =
-        __ldg(reinterpret_cast<const uint32_t*>(Q + br * blocks * 16 + g * 4));
-    const int k = g / 4;
-    const uint32_t sb = __ldg(S + (((b * tiles_r + r / 128) * tiles_c + k / 4) * 512 +
-                                   (r % 32) * 16 + (r % 128) / 32 * 4 + k % 4));
-    const float scale = sb == 0 ? __uint_as_float(0x00400000u)
-                                : __uint_as_float(sb == 255 ? 0x7fc00000u : sb << 23);
-    float v[8];
+  constexpr int V = BF16 ? 8 : 4;         // values per lane
+  constexpr int RW = V * 32 / QT;         // rows per warp access
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tc = static_cast<int>(blockIdx.x % tiles_c);
+  const int64_t br = blockIdx.x / tiles_c;
+  const int tr = static_cast<int>(br % tiles_r);
+  const int64_t b = br / tiles_r;
+  const int blocks = (cols + 31) / 32;
+  const int c = tc * QT + (lane * V) % QT;  // first column of this lane
+  if (c >= cols) return;
+  const uint8_t* tile = S + static_cast<int64_t>(blockIdx.x) * 512 + (c % QT) / 32;
+  const int64_t first = b * rows + tr * QT;
+  const uint8_t* q = Q + first * blocks * 16 + c / 2;
+  const int n = rows - tr * QT < QT ? rows - tr * QT : QT;
+  const bool wide = cols % V == 0;  // whole, aligned groups
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t c = codes >> (4 * j);
-      // exponent field 0: 0 or .5; otherwise (1 + m / 2) 2^(e - 1)
-      const uint32_t m = c & 7u;
-      const float a = m < 2 ? 0.5f * static_cast<float>(m)
-                            : __uint_as_float((((m >> 1) + 126u) << 23) | ((m & 1u) << 22));
-      v[j] = ((c & 8u) ? -a : a) * scale;
+  for (int half = 0; half < 2 / RW; ++half) {
+    uint32_t code[8], sb[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = (8 * (8 * half + i) + warp) * RW + lane * V / QT;
+      code[i] = sb[i] = 0;
+      if (r < n) {
+        const uint8_t* at = q + static_cast<int64_t>(r) * blocks * 16;
+        code[i] = BF16 ? __ldg(reinterpret_cast<const uint32_t*>(at))
+                       : __ldg(reinterpret_cast<const uint16_t*>(at));
+        sb[i] = __ldg(tile + (r & 31) * 16 + (r >> 5) * 4);
+      }
     }
-    const int64_t at = br * cols + g * 8;
-    if (BF16) {
-      uint32_t w[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-        w[j] = *reinterpret_cast<const uint32_t*>(&p);
-      }
-      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(X) + at;
-      if (cols % 8 == 0) {
-        *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < 8; ++i) {
+      const int r = (8 * (8 * half + i) + warp) * RW + lane * V / QT;
+      if (r >= n) continue;
+      const float scale = __uint_as_float(sb[i] == 0 ? 0x00400000u
+                                                     : (sb[i] == 255 ? 0x7fc00000u : sb[i] << 23));
+      float v[V];
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) e2m1x2(code[i] >> (8 * j), v[2 * j], v[2 * j + 1]);
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] *= scale;
+      const int64_t at = (first + r) * cols + c;
+      if (BF16) {
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(X) + at;
+        if (wide) {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * j], v[(2 * j + 1) % V]);
+            w[j] = *reinterpret_cast<const uint32_t*>(&x);
+          }
+          *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; ++j)
+            if (c + j < cols) o[j] = __float2bfloat16_rn(v[j]);
+        }
       } else {
-        for (int j = 0; j < 8 && g * 8 + j < cols; ++j) o[j] = __float2bfloat16_rn(v[j]);
-      }
-    } else {
-      float* o = static_cast<float*>(X) + at;
-      if (cols % 4 == 0) {
-        *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
-        if (g * 8 + 4 < cols) *reinterpret_cast<float4*>(o + 4) = make_float4(v[4], v[5], v[6], v[7]);
-      } else {
-        for (int j = 0; j < 8 && g * 8 + j < cols; ++j) o[j] = v[j];
+        float* o = static_cast<float*>(X) + at;
+        if (wide) {
+          *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; ++j)
+            if (c + j < cols) o[j] = v[j];
+        }
       }
     }
   }
@@ -546,28 +640,57 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
+namespace {
+
+template <bool BF16>
+cudaError_t launch_quantize(const CUtensorMap& x, const CUtensorMap& q, const CUtensorMap& qt,
+                            const QParams& p, cudaStream_t st) {
+  using C = QCfg<BF16>;
+  static_assert(C::SMEM <= 232448, "quantiser exceeds shared memory");
+  auto kern = k_mx4_quantize<BF16>;
+  static std::atomic<uint64_t> done{0};
+  const LaunchInfo li = launch_info(reinterpret_cast<const void*>(kern), C::SMEM, done);
+  if (li.err != cudaSuccess) return li.err;
+  const unsigned grid = static_cast<unsigned>(p.tiles < li.sms ? p.tiles : li.sms);
+  kern<<<grid, QTHREADS + 32, C::SMEM, st>>>(x, q, qt, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
 cudaError_t mx4_quantize(const void* X, bool bf16, int rows, int cols, int64_t batch, uint8_t* Q,
                          uint8_t* S, uint8_t* Qt, uint8_t* St, cudaStream_t st) {
-  const int tr = static_cast<int>(ceil_div(rows, QT)), tc = static_cast<int>(ceil_div(cols, QT));
-  const int64_t tiles = batch * tr * tc;
-  if (tiles > INT32_MAX) return cudaErrorInvalidValue;
-  auto kern = bf16 ? k_mx4_quantize<true> : k_mx4_quantize<false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, QSMEM);
-  if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(tiles), 256, QSMEM, st>>>(X, rows, cols, tr, tc, Mx4Out{Q, S},
-                                                         Mx4Out{Qt, St});
-  return cudaGetLastError();
+  QParams p;
+  p.rows = rows;
+  p.cols = cols;
+  p.tiles_r = static_cast<int>(ceil_div(rows, QT));
+  p.tiles_c = static_cast<int>(ceil_div(cols, QT));
+  p.tiles = batch * p.tiles_r * p.tiles_c;
+  p.s[0] = S;
+  p.s[1] = St;
+  // codes as 16-bit units: 8 per block of 32
+  const int64_t uc = ceil_div(cols, 32) * 8, ur = ceil_div(rows, 32) * 8;
+  CUtensorMap x, q, qt;
+  memset(&q, 0, sizeof(q));
+  memset(&qt, 0, sizeof(qt));
+  if (!tensor_map(&x, X, bf16 ? 2 : 4, cols, rows, batch, cols, static_cast<int64_t>(rows) * cols,
+                  bf16 ? 64 : 32, QT, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      (S != nullptr && !tensor_map(&q, Q, 2, uc, rows, batch, uc, uc * rows, 32, QT,
+                                   CU_TENSOR_MAP_SWIZZLE_64B)) ||
+      (St != nullptr && !tensor_map(&qt, Qt, 2, ur, cols, batch, ur, ur * cols, 32, QT,
+                                    CU_TENSOR_MAP_SWIZZLE_64B)))
+    return cudaErrorInvalidValue;
+  return bf16 ? launch_quantize<true>(x, q, qt, p, st) : launch_quantize<false>(x, q, qt, p, st);
 }
 
 cudaError_t mx4_dequantize(const uint8_t* Q, const uint8_t* S, int rows, int cols, int64_t batch,
                            void* X, bool bf16, cudaStream_t st) {
-  const int64_t n = batch * rows * ceil_div(cols, 8);
-  int64_t blocks = ceil_div(n, 256);
-  if (blocks > 148 * 64) blocks = 148 * 64;  // grid-stride: many waves per SM
+  const int tr = static_cast<int>(ceil_div(rows, QT)), tc = static_cast<int>(ceil_div(cols, QT));
+  const unsigned grid = static_cast<unsigned>(batch * tr * tc);
   if (bf16)
-    k_mx4_dequantize<true><<<static_cast<unsigned>(blocks), 256, 0, st>>>(Q, S, rows, cols, batch, X);
+    k_mx4_dequantize<true><<<grid, 256, 0, st>>>(Q, S, rows, cols, tr, tc, X);
   else
-    k_mx4_dequantize<false><<<static_cast<unsigned>(blocks), 256, 0, st>>>(Q, S, rows, cols, batch, X);
+    k_mx4_dequantize<false><<<grid, 256, 0, st>>>(Q, S, rows, cols, tr, tc, X);
   return cudaGetLastError();
 }
 
@@ -600,12 +723,10 @@ cudaError_t mx4_gemm(const uint8_t* A, const uint8_t* As, const uint8_t* B, cons
                   CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   auto kern = f32 ? k_mx4_gemm<true> : k_mx4_gemm<false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GSMEM);
-  if (e != cudaSuccess) return e;
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess)
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  int64_t ncl = sms / 2;
+  static std::atomic<uint64_t> done[2];
+  const LaunchInfo li = launch_info(reinterpret_cast<const void*>(kern), GSMEM, done[f32 ? 1 : 0]);
+  if (li.err != cudaSuccess) return li.err;
+  int64_t ncl = li.sms / 2;
   if (ncl > tiles) ncl = tiles;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * ncl), 1, 1);

@@ -301,12 +301,21 @@ def shp_matmul(Amat, B, prec="tf32", a_trans=False, b_trans=False, A_lo=None, B_
     return out
 
 
-def _on_current(*ts):
-    """The tensors share the current CUDA device (calls go to its current stream)."""
-    dev = torch.device("cuda", torch.cuda.current_device())
+def _ready(*ts):
+    """Checks that the tensors are contiguous and on the current CUDA device;
+    returns the handle of its current stream."""
     for t in ts:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensor on {t.device}, but the current device is {dev}")
+        if t is not None and not (t.is_cuda and t.is_contiguous()):
+            _dev(t)
+    dev = torch.cuda.current_device()
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _a(t):
+    return None if t is None else t.data_ptr()
 
 
 def _want(name, t, dtype, shape):
@@ -323,8 +332,7 @@ def shp_grouped_matmul(X, offsets, W, w_trans=False, out=None, dtype=torch.bfloa
     device; W: [groups, K, N] bf16 ([groups, N, K] with w_trans).  Y: `out`, or
     a new [T, N] tensor of `dtype` (bf16 or float32) whose rows outside every
     group are uninitialised; in `out` those rows are left as they were."""
-    _dev(X, offsets, W, out)
-    _on_current(X, offsets, W, out)
+    st = _ready(X, offsets, W, out)
     if X.dim() != 2 or W.dim() != 3 or offsets.dim() != 1:
         raise ValueError("X is [T, K], W [groups, K, N] and offsets [groups + 1]")
     T, K = X.shape
@@ -334,8 +342,8 @@ def shp_grouped_matmul(X, offsets, W, w_trans=False, out=None, dtype=torch.bfloa
     _want("offsets", offsets, torch.int64, (groups + 1,))
     out = torch.empty(T, N, dtype=dtype, device=X.device) if out is None else out
     _want("out", out, out.dtype, (T, N))
-    _check(A.lib().shp_grouped_matmul(_p(X), _p(offsets), _p(W), int(bool(w_trans)), _p(out),
-                                      _storage(out.dtype), T, K, N, groups, _stream()), "shp_grouped_matmul")
+    _check(A.lib().shp_grouped_matmul(_a(X), _a(offsets), _a(W), int(bool(w_trans)), _a(out),
+                                      _storage(out.dtype), T, K, N, groups, st), "shp_grouped_matmul")
     return out
 
 
@@ -346,8 +354,7 @@ def shp_grouped_wgrad(Amat, B, offsets, out=None, accumulate=False):
     A: [T, m], B: [T, n] bf16; offsets as in shp_grouped_matmul; G: `out`, or a
     new [groups, m, n] float32 tensor.  accumulate adds to `out` (which must
     then be given).  An empty group gives zeros, or leaves `out` as it is."""
-    _dev(Amat, B, offsets, out)
-    _on_current(Amat, B, offsets, out)
+    st = _ready(Amat, B, offsets, out)
     if Amat.dim() != 2 or B.dim() != 2 or offsets.dim() != 1 or offsets.shape[0] < 2:
         raise ValueError("A is [T, m], B [T, n] and offsets [groups + 1]")
     if accumulate and out is None:
@@ -359,8 +366,8 @@ def shp_grouped_wgrad(Amat, B, offsets, out=None, accumulate=False):
     _want("offsets", offsets, torch.int64, (groups + 1,))
     out = torch.empty(groups, m, n, dtype=torch.float32, device=B.device) if out is None else out
     _want("out", out, torch.float32, (groups, m, n))
-    _check(A.lib().shp_grouped_wgrad(_p(Amat), _p(B), _p(offsets), _p(out), T, m, n, groups,
-                                     int(bool(accumulate)), _stream()), "shp_grouped_wgrad")
+    _check(A.lib().shp_grouped_wgrad(_a(Amat), _a(B), _a(offsets), _a(out), T, m, n, groups,
+                                     int(bool(accumulate)), st), "shp_grouped_wgrad")
     return out
 
 
@@ -385,8 +392,7 @@ def shp_mx4_quantize(X, along="cols"):
     Qt, St) from one read of X.  Q: uint8 [batch, rows, Cp / 2], S: uint8
     [batch, rows / 128, cols / 128, 512] tiles (rounded up); layouts in the C
     header."""
-    _dev(X)
-    _on_current(X)
+    st = _ready(X)
     if along not in ("cols", "rows", "both") or X.dim() not in (2, 3):
         raise ValueError("X is [batch, rows, cols] or [rows, cols]; along is cols, rows or both")
     rows, cols = X.shape[-2], X.shape[-1]
@@ -394,15 +400,14 @@ def shp_mx4_quantize(X, along="cols"):
     new = lambda shapes: [torch.empty(s, dtype=torch.uint8, device=X.device) for s in shapes]  # noqa: E731
     q = new(_mx4_shapes(batch, rows, cols)) if along != "rows" else [None, None]
     qt = new(_mx4_shapes(batch, cols, rows)) if along != "cols" else [None, None]
-    _check(A.lib().shp_mx4_quantize(_p(X), _storage(X.dtype), rows, cols, batch, _p(q[0]), _p(q[1]),
-                                    _p(qt[0]), _p(qt[1]), _stream()), "shp_mx4_quantize")
+    _check(A.lib().shp_mx4_quantize(_a(X), _storage(X.dtype), rows, cols, batch, _a(q[0]), _a(q[1]),
+                                    _a(qt[0]), _a(qt[1]), st), "shp_mx4_quantize")
     return tuple(t for t in q + qt if t is not None)
 
 
 def shp_mx4_dequantize(Q, S, cols, dtype=torch.float32, out=None):
     """The values [batch, rows, cols] of MXFP4 codes and scales."""
-    _dev(Q, S, out)
-    _on_current(Q, S, out)
+    st = _ready(Q, S, out)
     if Q.dim() != 3:
         raise ValueError("Q is [batch, rows, Cp / 2]")
     batch, rows = Q.shape[0], Q.shape[1]
@@ -410,8 +415,8 @@ def shp_mx4_dequantize(Q, S, cols, dtype=torch.float32, out=None):
         _want(name, t, torch.uint8, shape)
     out = torch.empty(batch, rows, cols, dtype=dtype, device=Q.device) if out is None else out
     _want("out", out, out.dtype, (batch, rows, cols))
-    _check(A.lib().shp_mx4_dequantize(_p(Q), _p(S), rows, cols, batch, _p(out),
-                                      _storage(out.dtype), _stream()), "shp_mx4_dequantize")
+    _check(A.lib().shp_mx4_dequantize(_a(Q), _a(S), rows, cols, batch, _a(out),
+                                      _storage(out.dtype), st), "shp_mx4_dequantize")
     return out
 
 
@@ -419,8 +424,7 @@ def shp_mx4_matmul(Amat, A_scales, B, B_scales, dtype=torch.bfloat16, out=None):
     """C[b] = A[b] B[b]^T of two MXFP4 operands quantised along the contraction:
     A [batch, M, K / 2] and B [batch, N, K / 2] with their scale tiles.  C:
     `out`, or a new [batch, M, N] tensor of `dtype` (bf16 or float32)."""
-    _dev(Amat, A_scales, B, B_scales, out)
-    _on_current(Amat, A_scales, B, B_scales, out)
+    st = _ready(Amat, A_scales, B, B_scales, out)
     if Amat.dim() != 3 or B.dim() != 3:
         raise ValueError("A is [batch, M, K / 2] and B [batch, N, K / 2]")
     batch, M, K = Amat.shape[0], Amat.shape[1], Amat.shape[2] * 2
@@ -430,8 +434,8 @@ def shp_mx4_matmul(Amat, A_scales, B, B_scales, dtype=torch.bfloat16, out=None):
         _want(name, t, torch.uint8, shape)
     out = torch.empty(batch, M, N, dtype=dtype, device=B.device) if out is None else out
     _want("out", out, out.dtype, (batch, M, N))
-    _check(A.lib().shp_mx4_matmul(_p(Amat), _p(A_scales), _p(B), _p(B_scales), _p(out),
-                                  _storage(out.dtype), M, N, K, batch, _stream()),
+    _check(A.lib().shp_mx4_matmul(_a(Amat), _a(A_scales), _a(B), _a(B_scales), _a(out),
+                                  _storage(out.dtype), M, N, K, batch, st),
            "shp_mx4_matmul")
     return out
 
