@@ -1238,6 +1238,22 @@ bool tensor_map_rows(CUtensorMap* m, const float* ptr, int64_t inner, int64_t ro
                   CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+bool tensor_map4(CUtensorMap* m, const void* ptr, int esz, const int64_t (&dims)[4],
+                 const int64_t (&strides)[3], const int (&box)[4], CUtensorMapSwizzle swz) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t d[4], st[3];
+  cuuint32_t b[4], estr[4] = {1, 1, 1, 1};
+  for (int i = 0; i < 4; ++i) {
+    d[i] = static_cast<cuuint64_t>(dims[i]);
+    b[i] = static_cast<cuuint32_t>(box[i]);
+    if (i < 3) st[i] = static_cast<cuuint64_t>(strides[i] * esz);
+  }
+  return fn(m, esz == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4,
+            const_cast<void*>(ptr), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 LaunchInfo launch_info(const void* kernel, int smem, std::atomic<uint64_t>& done) {
   static std::atomic<int> sms[64];
   int dev = 0;

@@ -35,18 +35,14 @@ namespace shp {
 
 namespace {
 
-constexpr int ROWB = 128;                 // bytes of one row of a stage tile
-constexpr int BK = 64;                    // contraction elements per stage
-constexpr int A_BYTES = 128 * ROWB;       // per CTA: 128 rows (columns) of A ...
-constexpr int STAGE_BYTES = 2 * A_BYTES;  // ... and 128 of B
-constexpr int STAGES = 6;
-constexpr int BN = 256;
+constexpr int BK = 64;                // contraction elements per stage: 128-byte rows
+constexpr int A_BYTES = 128 * 128;    // per CTA and stage: 128 rows (columns) of A
 constexpr int CHUNK_KB = 8;  // stages per fp32 chunk: sums of 512 products inside the tensor core
 constexpr int EPI_WARPS = 8;
-constexpr int THREADS = 32 * (2 + EPI_WARPS + 1);
-constexpr int EPI_BOX = 4096;  // one warp's 32-row store box
-constexpr int GSMEM = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * EPI_BOX + 320;
-static_assert(GSMEM <= 232448, "grouped kernel exceeds shared memory");
+#ifndef NT_SMALL
+#define NT_SMALL 48
+#define NT_MID 128
+#endif
 
 SHP_DEV void tma_reduce_add_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
   asm volatile(
@@ -73,23 +69,31 @@ struct Groups {
   }
 };
 
-// Walks the row tiles of all groups in order.  find(t) is called by a whole
-// warp with increasing t and leaves the group and the tile's number within
-// it; 32 groups are looked at per step.
-struct RowTiles {
-  Groups g;
-  int rows_per_tile, tiles_n;
+// A tile of the rows product: `count` rows from row t0 in group e, weight
+// columns from n0.
+struct RowTile {
+  int e, t0, count, n0;
+};
+
+// Walks the tiles of all groups in order, every role of the kernel the same
+// sequence.  A group of len rows has ceil(len / NT) row tiles of equal size (up
+// to the MMA's granule of 16), each with every column tile.  next() is called
+// by whole warps and looks at 32 groups per step.
+template <int NT>
+struct RowWalk {
+  const Groups g;
+  const int tiles_n, step;
+  int t;
   int e0 = 0;    // first group of the window
   int base = 0;  // tiles before the window
-  int lo = 0, hi = 0, e = 0;
-  SHP_DEV bool find(int t, int& r) {
+  SHP_DEV RowWalk(const Groups& groups, int N, int first, int stride)
+      : g(groups), tiles_n((N + 255) / 256), step(stride), t(first) {}
+  SHP_DEV bool next(RowTile& x) {
     const int lane = threadIdx.x & 31;
     while (e0 < g.n) {
-      int a = 0, b = 0, cnt = 0;
-      if (e0 + lane < g.n) {
-        g.range(e0 + lane, a, b);
-        cnt = (b - a + rows_per_tile - 1) / rows_per_tile * tiles_n;
-      }
+      int a = 0, b = 0;
+      if (e0 + lane < g.n) g.range(e0 + lane, a, b);
+      const int cnt = (b - a + NT - 1) / NT * tiles_n;
       int inc = cnt;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -99,10 +103,15 @@ struct RowTiles {
       const unsigned in = __ballot_sync(0xffffffffu, t < base + inc);
       if (in != 0) {
         const int src = __ffs(in) - 1;
-        r = t - base - __shfl_sync(0xffffffffu, inc - cnt, src);
-        lo = __shfl_sync(0xffffffffu, a, src);
-        hi = __shfl_sync(0xffffffffu, b, src);
-        e = e0 + src;
+        const int r = t - base - __shfl_sync(0xffffffffu, inc - cnt, src);
+        const int lo = __shfl_sync(0xffffffffu, a, src), hi = __shfl_sync(0xffffffffu, b, src);
+        const int tiles = (hi - lo + NT - 1) / NT;
+        const int per = ((hi - lo + tiles - 1) / tiles + 15) & ~15;  // <= NT
+        x.e = e0 + src;
+        x.t0 = lo + r / tiles_n * per;
+        x.count = min(per, hi - x.t0);
+        x.n0 = r % tiles_n * 256;
+        t += step;
         return true;
       }
       base += __shfl_sync(0xffffffffu, inc, 31);
@@ -112,70 +121,314 @@ struct RowTiles {
   }
 };
 
-struct GroupedParams {
+// ---------------------------------------------------------- rows product
+//
+// k_grouped_rows computes the transposed tile, D (columns of W x rows of X):
+// the 256 columns of W are the MMA's M (128 per CTA of the pair) and the rows
+// of the group its N, any multiple of 16 up to NT.  So the time of the MMAs
+// follows the rows a group has, and few rows cost little more than streaming
+// W; with the rows as M = 256 a single row cost as much as 256.
+// NT (64, 128 or 256 rows) sets the ring: a stage is 16 KB of W and up to
+// NT * 64 bytes of X per CTA, so small tiles leave room for more stages of W in
+// flight.  The launcher picks it from the mean number of rows per group.
+// Epilogue: a lane holds one column of Y; for fp32 results 32 lanes store 128
+// contiguous bytes of a row, for bf16 lanes trade halves so that 16 lanes store
+// 64, directly and only inside the group.
+struct RowsParams {
   Groups g;
-  int M;  // wgrad: rows of G (columns of A); rows product: unused
   int N, K;
+  int w_chunks;  // W [K][N] is mapped as 64-column chunks: both of a CTA in one box
   void* out;
+};
+
+template <int NT>
+struct RowsCfg {
+  static constexpr int X_BYTES = NT / 2 * 128;
+  static constexpr int STAGE = A_BYTES + X_BYTES;
+  static constexpr int STAGES = (232448 - 1024 - 512) / STAGE;
+  static constexpr int SMEM = 1024 + STAGES * STAGE + 512;
+  static constexpr int THREADS = 32 * (2 + EPI_WARPS);
+};
+
+template <int NT, bool W_MN, bool F32>
+__global__ void __launch_bounds__(RowsCfg<NT>::THREADS, 1)
+    k_grouped_rows(const __grid_constant__ CUtensorMap tW, const __grid_constant__ CUtensorMap tX,
+                   const __grid_constant__ CUtensorMap tX32, RowsParams p) {
+  count_kernel_run();
+  using C = RowsCfg<NT>;
+  constexpr int STAGES = C::STAGES;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int ncl = static_cast<int>(gridDim.x) / 2, cl = static_cast<int>(blockIdx.x) / 2;
+  const int KB = (p.K + BK - 1) / BK;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * C::STAGE);
+  uint64_t* empty = full + STAGES;
+  uint64_t* accf = empty + STAGES;
+  uint64_t* acce = accf + 2;
+  uint64_t* drain = acce + 2;  // all MMAs of this pair complete
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(drain + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1) + 1;
+  static_assert((2 * STAGES + 5) * 8 + 8 <= 512, "barriers");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int u = 0; u < 2; ++u) {
+      mbar_init(&accf[u], 1);
+      mbar_init(&acce[u], 2 * EPI_WARPS);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tW);
+    tma_prefetch_desc(&tX);
+    tma_prefetch_desc(&tX32);
+  }
+  if (warp == 1) tmem_alloc_pair(tmem_slot, 2 * NT);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // peer barriers initialised, both TMEM allocations done
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  RowWalk<NT> walk(p.g, p.N, cl, ncl);
+  RowTile x;
+  if (warp == 0) {
+    // ---------------- TMA producer (both CTAs): its 128 columns of W and its
+    // half of the tile's rows, in boxes of 32
+    RingPos<STAGES> ring;
+    const uint32_t stages = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty);
+    const uint32_t fleader = mapa_shared(full0, 0);
+    bool stop = false;
+    while (!stop && walk.next(x)) {
+      const int n0 = x.n0 + static_cast<int>(rank) * 128;
+      const int half = ((x.count + 15) & ~15) / 2;  // rows per CTA
+      const int t0 = x.t0 + static_cast<int>(rank) * half;
+      // X in one box of NT / 2 rows, or in 32-row boxes where that moves less
+      const bool small = half <= NT / 4;
+      const int boxes = (half + 31) / 32;
+      const uint32_t tx = 2 * (A_BYTES + (small ? boxes * 4096u : C::X_BYTES));
+      if (lane == 0) {
+        for (int k0 = 0; k0 < p.K; k0 += BK) {
+          if (!ring_wait(empty0 + ring.slot * 8, ring.parity ^ 1u, abort_flag)) {
+            stop = true;
+            break;
+          }
+          const uint32_t sw = stages + ring.slot * C::STAGE, sx = sw + A_BYTES;
+          const uint32_t fbar = fleader + ring.slot * 8;
+          if (leader) mbar_expect_tx_u32(full0 + ring.slot * 8, tx);
+          if (W_MN && p.w_chunks) {
+            tma_4d_pair(sw, &tW, fbar, 0, k0, n0 >> 6, x.e);
+          } else if (W_MN) {
+            tma_3d_pair(sw, &tW, fbar, n0, k0, x.e);
+            tma_3d_pair(sw + BK * 128, &tW, fbar, n0 + 64, k0, x.e);
+          } else {
+            tma_3d_pair(sw, &tW, fbar, k0, n0, x.e);
+          }
+          if (!small) {
+            tma_3d_pair(sx, &tX, fbar, k0, t0, 0);
+          } else {
+            for (int i = 0; i < boxes; ++i)
+              tma_3d_pair(sx + i * 4096, &tX32, fbar, k0, t0 + i * 32, 0);
+          }
+          ring.advance();
+        }
+      }
+      stop = __shfl_sync(0xffffffffu, stop ? 1 : 0, 0) != 0;
+    }
+    // a wait that gave up leaves copies in flight that no MMA waits for: let
+    // them land (bounded) before the CTAs exit
+    if (stop && leader && lane == 0) {
+      for (int k = 0; k < STAGES; ++k, ring.advance()) mbar_wait(&full[ring.slot], ring.parity ^ 1u);
+    }
+  } else if (warp == 1) {
+    if (leader) {
+      // ---------------- MMA issuer (leader of the pair)
+      RingPos<STAGES> ring;
+      RingPos<2> au;  // accumulator
+      const uint32_t full0 = smem_u32(full), acce0 = smem_u32(acce);
+      const uint64_t wdesc = W_MN ? smem_desc(smem_u32(smem), BK * 128, 1024u, 2u)
+                                  : smem_desc(smem_u32(smem), 16, 1024u, 2u);
+      const uint64_t xdesc = smem_desc(smem_u32(smem) + A_BYTES, 16, 1024u, 2u);
+      constexpr uint64_t WSTEP = (W_MN ? 16 * 128 : 32) >> 4, XSTEP = 32 >> 4;
+      bool stop = false;
+      while (!stop && walk.next(x)) {
+        if (lane == 0) {
+          const uint32_t idesc = instr_desc(1u, W_MN, false, 256, (x.count + 15) & ~15);
+          for (int c0 = 0; c0 < KB && !stop; c0 += F32 ? CHUNK_KB : KB, au.advance()) {
+            const int c1 = F32 ? min(c0 + CHUNK_KB, KB) : KB;
+            if (!ring_wait(acce0 + au.slot * 8, au.parity ^ 1u, abort_flag)) {
+              stop = true;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t dacc = tmem + au.slot * NT;
+            for (int kb = c0; kb < c1; ++kb) {
+              if (!ring_wait(full0 + ring.slot * 8, ring.parity, abort_flag)) {
+                stop = true;
+                break;
+              }
+              tc_fence_after();
+              const uint64_t at = static_cast<uint64_t>(ring.slot) * (C::STAGE >> 4);
+#pragma unroll
+              for (int ks = 0; ks < BK / 16; ++ks)
+                mma_f16_pair(dacc, wdesc + at + ks * WSTEP, xdesc + at + ks * XSTEP, idesc,
+                             (kb > c0 || ks > 0) ? 1u : 0u);
+              mma_commit_pair(&empty[ring.slot], 3);
+              ring.advance();
+            }
+            mma_commit_pair(&accf[au.slot], 3);
+          }
+        }
+        stop = __shfl_sync(0xffffffffu, stop ? 1 : 0, 0) != 0;
+      }
+      if (lane == 0) mma_commit_pair(drain, 3);  // after every MMA issued above
+    }
+  } else {
+    // ---------------- epilogue warps (both CTAs, each on its TMEM rows): warp
+    // (q, h) takes the W columns of lane quarter q and the 32-row chunks
+    // h, h + 2, ... of the tile
+    constexpr int NC = NT / 64;  // chunks per warp
+    const int q = warp & 3, h = (warp - 2) >> 2;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    int it = 0;
+    bool stop = false;
+    while (!stop && walk.next(x)) {
+      const int nb = x.n0 + static_cast<int>(rank) * 128 + q * 32;  // this warp's first column
+      if (F32) {
+        float acc[NC * 32];
+#pragma unroll
+        for (int j = 0; j < NC * 32; ++j) acc[j] = 0.f;
+        for (int c0 = 0; c0 < KB; c0 += CHUNK_KB, ++it) {
+          const int u = it & 1;
+          if (!warp_wait(&accf[u], (it >> 1) & 1, abort_flag)) {
+            stop = true;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            if ((2 * c + h) * 32 < x.count) {
+              float v[32];
+              tmem_ld32(trow + static_cast<uint32_t>(u * NT + (2 * c + h) * 32), v);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) acc[c * 32 + j] += v[j];
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acce[u]), 0));
+        }
+        if (stop) break;
+        if (nb + lane < p.N) {
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const int r0 = (2 * c + h) * 32;
+            float* o = static_cast<float*>(p.out) + static_cast<int64_t>(x.t0 + r0) * p.N + nb + lane;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (r0 + j < x.count) o[static_cast<int64_t>(j) * p.N] = acc[c * 32 + j];
+          }
+        }
+      } else {
+        const int u = it & 1;
+        if (!warp_wait(&accf[u], (it >> 1) & 1, abort_flag)) break;
+        ++it;
+        tc_fence_after();
+        // lane l stores columns nb + (l & ~1), + 1 of the even (odd) rows
+        const int odd = lane & 1;
+        const bool in = nb + lane < p.N;  // N is even: a pair is in or out
+#pragma unroll 1
+        for (int r0 = h * 32; r0 < x.count; r0 += 64) {
+          float v[32];
+          tmem_ld32(trow + static_cast<uint32_t>(u * NT + r0), v);
+          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) +
+                             static_cast<int64_t>(x.t0 + r0 + odd) * p.N + nb + lane - odd;
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+            const __nv_bfloat162 w = odd ? __floats2bfloat162_rn(got, v[j + 1])
+                                         : __floats2bfloat162_rn(v[j], got);
+            if (in && r0 + j + odd < x.count)
+              *reinterpret_cast<__nv_bfloat162*>(o + static_cast<int64_t>(j) * p.N) = w;
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acce[u]), 0));
+      }
+    }
+  }
+
+  if (warp == 1) mbar_wait(drain, 0);  // bounded; immediate unless a wait above gave up
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) tmem_dealloc_pair(tmem, 2 * NT);
+}
+
+// -------------------------------------------------------- weight gradient
+//
+// k_grouped_wgrad: 256 x 256 tiles of G_e, both operands MN-major (rows of A
+// and B are the contraction), a 128-column half of each per CTA.
+
+constexpr int STAGE_BYTES = 2 * A_BYTES;
+constexpr int STAGES = 6;
+constexpr int BN = 256;
+constexpr int THREADS = 32 * (2 + EPI_WARPS + 1);
+constexpr int EPI_BOX = 4096;  // one warp's 32-row store box
+constexpr int GSMEM = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * EPI_BOX + 320;
+static_assert(GSMEM <= 232448, "weight-gradient kernel exceeds shared memory");
+
+struct WgradParams {
+  Groups g;
+  int M, N;
   int accumulate;
+  int chunks;  // tA2, tB2 bring both 64-column chunks of a CTA in one box
 };
 
-// One tile: group e, tile rows from m0 (a row of X, or a row of G), columns
-// from n0, `kb` stages of contraction starting at row / column k0; `tail`
-// valid rows in the last stage (0: all 64).
+// One tile: group e, tile (m0, n0), kb stages from row k0; `tail` valid rows in
+// the last stage (0: all 64).
 struct Tile {
-  int e, m0, n0, k0, kb, tail, mend;
+  int e, m0, n0, k0, kb, tail;
 };
 
-// The tiles of a CTA pair in order; every role of the kernel walks the same
-// sequence.  Called by whole warps.
-template <bool WG>
 struct Walk {
-  const GroupedParams& p;
-  RowTiles rt;
+  const WgradParams& p;
   int t, step, tiles_n, per_e;
-  SHP_DEV Walk(const GroupedParams& q, int first, int stride) : p(q), t(first), step(stride) {
+  SHP_DEV Walk(const WgradParams& q, int first, int stride) : p(q), t(first), step(stride) {
     tiles_n = (q.N + BN - 1) / BN;
     per_e = tiles_n * ((q.M + 255) / 256);
-    rt.g = q.g;
-    rt.rows_per_tile = 256;
-    rt.tiles_n = tiles_n;
   }
   SHP_DEV bool next(Tile& x) {
-    if (WG) {
-      if (t >= per_e * p.g.n) return false;
-      x.e = t / per_e;
-      const int r = t % per_e;
-      int lo, hi;
-      p.g.range(x.e, lo, hi);
-      x.m0 = r / tiles_n * 256;
-      x.mend = p.M;
-      x.n0 = r % tiles_n * BN;
-      x.k0 = lo;
-      x.kb = (hi - lo + BK - 1) / BK;
-      x.tail = (hi - lo) % BK;
-    } else {
-      int r;
-      if (!rt.find(t, r)) return false;
-      x.e = rt.e;
-      x.m0 = rt.lo + r / tiles_n * 256;
-      x.mend = rt.hi;
-      x.n0 = r % tiles_n * BN;
-      x.k0 = 0;
-      x.kb = (p.K + BK - 1) / BK;
-      x.tail = 0;
-    }
+    if (t >= per_e * p.g.n) return false;
+    x.e = t / per_e;
+    const int r = t % per_e;
+    int lo, hi;
+    p.g.range(x.e, lo, hi);
+    x.m0 = r / tiles_n * 256;
+    x.n0 = r % tiles_n * BN;
+    x.k0 = lo;
+    x.kb = (hi - lo + BK - 1) / BK;
+    x.tail = (hi - lo) % BK;
     t += step;
     return true;
   }
 };
 
-template <bool WG, bool B_MN, bool F32>
 __global__ void __launch_bounds__(THREADS, 1)
-    k_grouped(const __grid_constant__ CUtensorMap tA, const __grid_constant__ CUtensorMap tB,
-              const __grid_constant__ CUtensorMap tO, GroupedParams p) {
+    k_grouped_wgrad(const __grid_constant__ CUtensorMap tA, const __grid_constant__ CUtensorMap tB,
+                    const __grid_constant__ CUtensorMap tA2,
+                    const __grid_constant__ CUtensorMap tB2,
+                    const __grid_constant__ CUtensorMap tO, WgradParams p) {
   count_kernel_run();
-  constexpr bool A_MN = WG;
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
   const int ncl = static_cast<int>(gridDim.x) / 2, cl = static_cast<int>(blockIdx.x) / 2;
@@ -209,8 +462,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
-    tma_prefetch_desc(&tA);
-    tma_prefetch_desc(&tB);
+    tma_prefetch_desc(p.chunks ? &tA2 : &tA);
+    tma_prefetch_desc(p.chunks ? &tB2 : &tB);
     tma_prefetch_desc(&tO);
   }
   if (warp == 1) tmem_alloc_pair(tmem_slot, 2 * BN);
@@ -220,51 +473,49 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  Walk<WG> walk(p, cl, ncl);
+  Walk walk(p, cl, ncl);
   Tile x;
   if (warp == 0) {
     // ---------------- TMA producer (both CTAs)
-    int kit = 0;
+    RingPos<STAGES> ring;
+    const uint32_t stages = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty);
+    const uint32_t fleader = mapa_shared(full0, 0);
     bool stop = false;
     while (!stop && walk.next(x)) {
       const int m0 = x.m0 + static_cast<int>(rank) * 128;
       const int nb0 = x.n0 + static_cast<int>(rank) * 128;
+      const int whole = x.kb - (x.tail != 0 ? 1 : 0);  // stages without a tail
       if (lane == 0) {
-        for (int kb = 0; kb < x.kb; ++kb, ++kit) {
-          const int s = kit % STAGES;
-          if (kit >= STAGES &&
-              (*abort_flag || !mbar_wait(&empty[s], ((kit / STAGES) - 1) & 1, abort_flag))) {
-            *abort_flag = 1;
+        for (int kb = 0; kb < x.kb; ++kb) {
+          if (!ring_wait(empty0 + ring.slot * 8, ring.parity ^ 1u, abort_flag)) {
             stop = true;
             break;
           }
-          uint8_t* sa = smem + s * STAGE_BYTES;
-          uint8_t* sb = sa + A_BYTES;
+          const uint32_t sa = stages + ring.slot * STAGE_BYTES, sb = sa + A_BYTES;
           const int k0 = x.k0 + kb * BK;
-          if (WG && x.tail != 0 && kb == x.kb - 1) {
+          if (kb >= whole) {
             // partial stage: this CTA's halves, for the clearing warp
-            mbar_arrive_expect_tx(&tailb[s], STAGE_BYTES);
+            uint64_t* bar = &tailb[ring.slot];
+            uint8_t* st = smem + ring.slot * STAGE_BYTES;
+            mbar_arrive_expect_tx(bar, STAGE_BYTES);
             for (int i = 0; i < 2; ++i) {
-              tma_load_3d(sa + i * BK * 128, &tA, &tailb[s], m0 + i * 64, k0, 0);
-              tma_load_3d(sb + i * BK * 128, &tB, &tailb[s], nb0 + i * 64, k0, 0);
+              tma_load_3d(st + i * BK * 128, &tA, bar, m0 + i * 64, k0, 0);
+              tma_load_3d(st + A_BYTES + i * BK * 128, &tB, bar, nb0 + i * 64, k0, 0);
             }
-            continue;
-          }
-          const uint32_t fbar = mapa_shared(smem_u32(&full[s]), 0);
-          if (leader) mbar_arrive_expect_tx(&full[s], 2 * STAGE_BYTES);
-          if (A_MN) {
-            for (int i = 0; i < 2; ++i)
-              tma_load_3d_pair(sa + i * BK * 128, &tA, fbar, m0 + i * 64, k0, 0);
           } else {
-            tma_load_3d_pair(sa, &tA, fbar, k0, m0, 0);
+            const uint32_t fbar = fleader + ring.slot * 8;
+            if (leader) mbar_expect_tx_u32(full0 + ring.slot * 8, 2 * STAGE_BYTES);
+            if (p.chunks) {
+              tma_4d_pair(sa, &tA2, fbar, 0, k0, m0 >> 6, 0);
+              tma_4d_pair(sb, &tB2, fbar, 0, k0, nb0 >> 6, 0);
+            } else {
+              for (int i = 0; i < 2; ++i) {
+                tma_3d_pair(sa + i * BK * 128, &tA, fbar, m0 + i * 64, k0, 0);
+                tma_3d_pair(sb + i * BK * 128, &tB, fbar, nb0 + i * 64, k0, 0);
+              }
+            }
           }
-          const int eb = WG ? 0 : x.e;
-          if (B_MN) {
-            for (int i = 0; i < 2; ++i)
-              tma_load_3d_pair(sb + i * BK * 128, &tB, fbar, nb0 + i * 64, k0, eb);
-          } else {
-            tma_load_3d_pair(sb, &tB, fbar, k0, nb0, eb);
-          }
+          ring.advance();
         }
       }
       stop = __shfl_sync(0xffffffffu, stop ? 1 : 0, 0) != 0;
@@ -272,54 +523,53 @@ __global__ void __launch_bounds__(THREADS, 1)
     // a wait that gave up leaves copies in flight that no MMA waits for: let
     // them land (bounded) before the CTAs exit
     if (stop && leader && lane == 0) {
-      for (int k = kit > STAGES ? kit - STAGES : 0; k < kit; ++k)
-        mbar_wait(&full[k % STAGES], (k / STAGES) & 1);
+      for (int k = 0; k < STAGES; ++k, ring.advance()) mbar_wait(&full[ring.slot], ring.parity ^ 1u);
     }
   } else if (warp == 1) {
     if (leader) {
       // ---------------- MMA issuer (leader of the pair)
-      const uint32_t idesc = instr_desc(1u, A_MN, B_MN, 256, BN);
-      const uint32_t mn_lbo = BK * 128;
-      int kit = 0, it = 0;  // stages and accumulator chunks so far
+      const uint32_t idesc = instr_desc(1u, true, true, 256, BN);
+      RingPos<STAGES> ring;
+      RingPos<2> au;  // accumulator
+      const uint32_t full0 = smem_u32(full), acce0 = smem_u32(acce);
+      const uint64_t adesc = smem_desc(smem_u32(smem), BK * 128, 1024u, 2u);
+      const uint64_t bdesc = smem_desc(smem_u32(smem) + A_BYTES, BK * 128, 1024u, 2u);
+      constexpr uint64_t KSTEP = 16 * 128 >> 4;
       bool stop = false;
       while (!stop && walk.next(x)) {
         if (lane == 0) {
-          for (int c0 = 0; c0 < x.kb && !stop; c0 += F32 ? CHUNK_KB : x.kb, ++it) {
-            const int c1 = F32 ? min(c0 + CHUNK_KB, x.kb) : x.kb;
-            const int u = it & 1, use = it >> 1;
-            if (use >= 1 && (*abort_flag || !mbar_wait(&acce[u], (use - 1) & 1, abort_flag))) {
-              *abort_flag = 1;
+          const int whole = x.kb - (x.tail != 0 ? 1 : 0);
+          for (int c0 = 0; c0 < x.kb && !stop; c0 += CHUNK_KB, au.advance()) {
+            const int c1 = min(c0 + CHUNK_KB, x.kb);
+            if (!ring_wait(acce0 + au.slot * 8, au.parity ^ 1u, abort_flag)) {
               stop = true;
               break;
             }
             tc_fence_after();
-            const uint32_t dacc = tmem + static_cast<uint32_t>(u * BN);
-            for (int kb = c0; kb < c1; ++kb, ++kit) {
-              const int s = kit % STAGES;
-              if (*abort_flag || !mbar_wait(&full[s], (kit / STAGES) & 1, abort_flag)) {
-                *abort_flag = 1;
+            const uint32_t dacc = tmem + au.slot * BN;
+            for (int kb = c0; kb < c1; ++kb) {
+              if (!ring_wait(full0 + ring.slot * 8, ring.parity, abort_flag)) {
                 stop = true;
                 break;
               }
-              int steps = BK / 16;
-              if (WG && x.tail != 0 && kb == x.kb - 1) {
-                steps = (x.tail + 15) / 16;
-                fence_cluster();  // the peer's half was cleared by its own warp
-              }
-              tc_fence_after();
-              const uint32_t sa = smem_u32(smem + s * STAGE_BYTES), sb = sa + A_BYTES;
+              const uint64_t at = static_cast<uint64_t>(ring.slot) * (STAGE_BYTES >> 4);
+              if (kb < whole) {
+                tc_fence_after();
 #pragma unroll
-              for (int ks = 0; ks < BK / 16; ++ks) {
-                if (WG && ks >= steps) break;
-                const uint64_t ad = A_MN ? smem_desc(sa + ks * 16 * 128, mn_lbo, 1024u, 2u)
-                                         : smem_desc(sa + ks * 32, 16, 1024u, 2u);
-                const uint64_t bd = B_MN ? smem_desc(sb + ks * 16 * 128, mn_lbo, 1024u, 2u)
-                                         : smem_desc(sb + ks * 32, 16, 1024u, 2u);
-                mma_f16_pair(dacc, ad, bd, idesc, (kb > c0 || ks > 0) ? 1u : 0u);
+                for (int ks = 0; ks < BK / 16; ++ks)
+                  mma_f16_pair(dacc, adesc + at + ks * KSTEP, bdesc + at + ks * KSTEP, idesc,
+                               (kb > c0 || ks > 0) ? 1u : 0u);
+              } else {
+                fence_cluster();  // the peer's half was cleared by its own warp
+                tc_fence_after();
+                for (int ks = 0; ks < (x.tail + 15) / 16; ++ks)
+                  mma_f16_pair(dacc, adesc + at + ks * KSTEP, bdesc + at + ks * KSTEP, idesc,
+                               (kb > c0 || ks > 0) ? 1u : 0u);
               }
-              mma_commit_pair(&empty[s], 3);
+              mma_commit_pair(&empty[ring.slot], 3);
+              ring.advance();
             }
-            mma_commit_pair(&accf[u], 3);
+            mma_commit_pair(&accf[au.slot], 3);
           }
         }
         stop = __shfl_sync(0xffffffffu, stop ? 1 : 0, 0) != 0;
@@ -336,10 +586,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     while (!stop && walk.next(x)) {
       const int row0 = x.m0 + static_cast<int>(rank) * 128 + q * 32;
       const int c0 = x.n0 + h * 128;
-      const int row = row0 + lane;
-      const bool whole = WG ? row0 < x.mend : row0 + 32 <= x.mend;  // a box store covers it
-      const int64_t rbase = static_cast<int64_t>(row) * p.N;
-      if (F32) {
         float acc[128];
 #pragma unroll
         for (int j = 0; j < 128; ++j) acc[j] = 0.f;
@@ -363,92 +609,33 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acce[u]), 0));
         }
         if (stop) break;
-        if (WG && p.accumulate && nc == 0) continue;  // an empty group leaves G as it is
+        if (p.accumulate && nc == 0) continue;  // an empty group leaves G as it is
+        if (row0 >= p.M) continue;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const int cb = c0 + g * 32;
-          if (cb < p.N) {
-            if (whole) {
-              if (lane == 0) bulk_wait_read_all();  // the previous store has read the box
-              __syncwarp();
+          if (cb >= p.N) continue;
+          if (lane == 0) bulk_wait_read_all();  // the previous store has read the box
+          __syncwarp();
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<float4*>(box + sw128_off(lane, i)) =
-                    make_float4(acc[g * 32 + 4 * i], acc[g * 32 + 4 * i + 1],
-                                acc[g * 32 + 4 * i + 2], acc[g * 32 + 4 * i + 3]);
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                if (WG && p.accumulate)
-                  tma_reduce_add_3d(&tO, box, cb, row0, x.e);
-                else
-                  tma_store_3d(&tO, box, cb, row0, WG ? x.e : 0);
-                bulk_commit();
-              }
-            } else if (!WG && row < x.mend) {
-              float* o = static_cast<float*>(p.out) + rbase + cb;
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (cb + 4 * i < p.N)
-                  *reinterpret_cast<float4*>(o + 4 * i) =
-                      make_float4(acc[g * 32 + 4 * i], acc[g * 32 + 4 * i + 1],
-                                  acc[g * 32 + 4 * i + 2], acc[g * 32 + 4 * i + 3]);
-            }
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(box + sw128_off(lane, i)) =
+                make_float4(acc[g * 32 + 4 * i], acc[g * 32 + 4 * i + 1], acc[g * 32 + 4 * i + 2],
+                            acc[g * 32 + 4 * i + 3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (p.accumulate)
+              tma_reduce_add_3d(&tO, box, cb, row0, x.e);
+            else
+              tma_store_3d(&tO, box, cb, row0, x.e);
+            bulk_commit();
           }
         }
-      } else {
-        const int u = it & 1;
-        if (!warp_wait(&accf[u], (it >> 1) & 1, abort_flag)) break;
-        ++it;
-        tc_fence_after();
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const int cb = c0 + g * 64;
-          uint32_t w[32];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float v[32];
-            tmem_ld32(trow + static_cast<uint32_t>(u * BN + g * 64 + k * 32), v);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-              w[16 * k + j] = *reinterpret_cast<const uint32_t*>(&t);
-            }
-          }
-          if (g == 1) {  // the accumulator is in registers: hand it back
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acce[u]), 0));
-          }
-          if (cb < p.N) {
-            if (whole) {
-              if (lane == 0) bulk_wait_read_all();
-              __syncwarp();
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<uint4*>(box + sw128_off(lane, i)) =
-                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                tma_store_3d(&tO, box, cb, row0, 0);
-                bulk_commit();
-              }
-            } else if (row < x.mend) {
-              __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + rbase + cb;
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (cb + 8 * i < p.N)
-                  *reinterpret_cast<uint4*>(o + 8 * i) =
-                      make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-            }
-          }
-        }
-      }
     }
     if (lane == 0) bulk_wait_all();  // nothing outlives the CTA's shared memory
     __syncwarp();
-  } else if (WG) {
+  } else {
     // ---------------- clearing warp: rows behind the group in its last stage
     int kit = 0;
     uint32_t par = 0;  // phase of each stage's tailb and clearb
@@ -487,58 +674,82 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp == 1) tmem_dealloc_pair(tmem, 2 * BN);
 }
 
-template <bool WG, bool B_MN, bool F32>
-cudaError_t launch_grouped(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
-                           const GroupedParams& p, int64_t max_tiles, cudaStream_t st) {
-  auto kern = k_grouped<WG, B_MN, F32>;
-  static std::atomic<uint64_t> done{0};
-  const LaunchInfo li = launch_info(reinterpret_cast<const void*>(kern), GSMEM, done);
-  if (li.err != cudaSuccess) return li.err;
-  int64_t ncl = li.sms / 2;
+// A launch of one CTA pair per SM pair, or fewer for fewer tiles.
+cudaLaunchConfig_t pair_grid(int sms, int64_t max_tiles, int threads, int smem, cudaStream_t st,
+                             cudaLaunchAttribute* attr) {
+  int64_t ncl = sms / 2;
   if (ncl > max_tiles) ncl = max_tiles;
   if (ncl < 1) ncl = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * ncl), 1, 1);
-  cfg.blockDim = dim3(THREADS, 1, 1);
-  cfg.dynamicSmemBytes = GSMEM;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = 2;
+  attr->val.clusterDim.y = 1;
+  attr->val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, a, b, o, p);
+  return cfg;
+}
+
+template <int NT, bool W_MN, bool F32>
+cudaError_t launch_rows(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& x32,
+                        const RowsParams& p, int T, cudaStream_t st) {
+  using C = RowsCfg<NT>;
+  auto kern = k_grouped_rows<NT, W_MN, F32>;
+  static std::atomic<uint64_t> done{0};
+  const LaunchInfo li = launch_info(reinterpret_cast<const void*>(kern), C::SMEM, done);
+  if (li.err != cudaSuccess) return li.err;
+  // every group has at most one row tile more than its share of full ones
+  const int64_t tiles = (T / NT + static_cast<int64_t>(p.g.n < T ? p.g.n : T)) * ((p.N + 255) / 256);
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg = pair_grid(li.sms, tiles, C::THREADS, C::SMEM, st, &attr);
+  return cudaLaunchKernelEx(&cfg, kern, w, x, x32, p);
+}
+
+template <int NT>
+cudaError_t dispatch_rows(const void* X, const CUtensorMap& w, bool w_mn, bool f32,
+                          const RowsParams& p, int T, cudaStream_t st) {
+  CUtensorMap x, x32;
+  if (!tensor_map(&x, X, 2, p.K, T, 1, p.K, 0, BK, NT / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !tensor_map(&x32, X, 2, p.K, T, 1, p.K, 0, BK, 32, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  if (w_mn)
+    return f32 ? launch_rows<NT, true, true>(w, x, x32, p, T, st)
+               : launch_rows<NT, true, false>(w, x, x32, p, T, st);
+  return f32 ? launch_rows<NT, false, true>(w, x, x32, p, T, st)
+             : launch_rows<NT, false, false>(w, x, x32, p, T, st);
 }
 
 }  // namespace
 
 cudaError_t grouped_rows(const void* X, const int64_t* offsets, const void* W, bool w_trans,
                          void* Y, int T, int K, int N, int groups, bool f32, cudaStream_t st) {
-  CUtensorMap a, b, o;
-  const int64_t kn = static_cast<int64_t>(K) * N;
-  bool ok = tensor_map(&a, X, 2, K, T, 1, K, 0, BK, 128, CU_TENSOR_MAP_SWIZZLE_128B);
-  ok = ok && (w_trans ? tensor_map(&b, W, 2, K, N, groups, K, kn, BK, 128,
-                                   CU_TENSOR_MAP_SWIZZLE_128B)
-                      : tensor_map(&b, W, 2, N, K, groups, N, kn, 64, BK,
-                                   CU_TENSOR_MAP_SWIZZLE_128B));
-  ok = ok && tensor_map(&o, Y, f32 ? 4 : 2, N, T, 1, N, 0, f32 ? 32 : 64, 32,
-                        CU_TENSOR_MAP_SWIZZLE_128B);
-  if (!ok) return cudaErrorInvalidValue;
-  GroupedParams p;
+  RowsParams p;
   memset(&p, 0, sizeof(p));
   p.g = Groups{offsets, groups, T};
   p.N = N;
   p.K = K;
   p.out = Y;
-  // every group has at most one partial tile
-  const int64_t tiles = (T / 256 + static_cast<int64_t>(groups < T ? groups : T)) * ((N + BN - 1) / BN);
-  if (w_trans)
-    return f32 ? launch_grouped<false, false, true>(a, b, o, p, tiles, st)
-               : launch_grouped<false, false, false>(a, b, o, p, tiles, st);
-  return f32 ? launch_grouped<false, true, true>(a, b, o, p, tiles, st)
-             : launch_grouped<false, true, false>(a, b, o, p, tiles, st);
+  CUtensorMap w;
+  const int64_t kn = static_cast<int64_t>(K) * N;
+  bool ok;
+  if (w_trans) {
+    ok = tensor_map(&w, W, 2, K, N, groups, K, kn, BK, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+  } else if (N % 64 == 0) {
+    p.w_chunks = 1;
+    ok = tensor_map4(&w, W, 2, {64, K, N / 64, groups}, {N, 64, kn}, {64, BK, 2, 1},
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+  } else {
+    ok = tensor_map(&w, W, 2, N, K, groups, N, kn, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B);
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  const int64_t mean = T / groups;
+  if (mean <= NT_SMALL) return dispatch_rows<64>(X, w, !w_trans, f32, p, T, st);
+  if (mean <= NT_MID) return dispatch_rows<128>(X, w, !w_trans, f32, p, T, st);
+  return dispatch_rows<256>(X, w, !w_trans, f32, p, T, st);
 }
 
 cudaError_t grouped_wgrad(const void* A, const void* B, const int64_t* offsets, float* G, int T,
@@ -553,15 +764,28 @@ cudaError_t grouped_wgrad(const void* A, const void* B, const int64_t* offsets, 
                         CU_TENSOR_MAP_SWIZZLE_128B);
   if (!ok) return cudaErrorInvalidValue;
   if (T == 0) a = b = o;  // no group has a row: never loaded from
-  GroupedParams p;
+  WgradParams p;
   memset(&p, 0, sizeof(p));
+  CUtensorMap a2 = a, b2 = b;
+  if (T > 0 && M % 64 == 0 && N % 64 == 0) {
+    p.chunks = 1;
+    if (!tensor_map4(&a2, A, 2, {64, T, M / 64, 1}, {M, 64, static_cast<int64_t>(T) * M},
+                     {64, BK, 2, 1}, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !tensor_map4(&b2, B, 2, {64, T, N / 64, 1}, {N, 64, static_cast<int64_t>(T) * N},
+                     {64, BK, 2, 1}, CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  }
   p.g = Groups{offsets, groups, T};
   p.M = M;
   p.N = N;
-  p.out = G;
   p.accumulate = accumulate ? 1 : 0;
   const int64_t tiles = static_cast<int64_t>(groups) * ((M + 255) / 256) * ((N + BN - 1) / BN);
-  return launch_grouped<true, true, true>(a, b, o, p, tiles, st);
+  static std::atomic<uint64_t> done{0};
+  const LaunchInfo li = launch_info(reinterpret_cast<const void*>(k_grouped_wgrad), GSMEM, done);
+  if (li.err != cudaSuccess) return li.err;
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg = pair_grid(li.sms, tiles, THREADS, GSMEM, st, &attr);
+  return cudaLaunchKernelEx(&cfg, k_grouped_wgrad, a, b, a2, b2, o, p);
 }
 
 uint64_t kernel_runs_grouped() {

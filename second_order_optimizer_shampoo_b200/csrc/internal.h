@@ -120,6 +120,11 @@ bool tensor_map(CUtensorMap* m, const void* ptr, int esz, int64_t inner, int64_t
                 int64_t batch, int64_t ld, int64_t bstride, int box_inner, int box_rows,
                 CUtensorMapSwizzle swz);
 
+// 4-D map of 2- or 4-byte elements (copied bit for bit): dims and box from the
+// innermost dimension on, strides of dimensions 1..3 in elements.
+bool tensor_map4(CUtensorMap* m, const void* ptr, int esz, const int64_t (&dims)[4],
+                 const int64_t (&strides)[3], const int (&box)[4], CUtensorMapSwizzle swz);
+
 // 4-D int8 map over [blocks][slices][rows][kb_bytes] (the K-blocked digit
 // slices of the Ozaki-scheme products, ozaki.cu; kb_bytes 64 or 128) with a
 // box of all slices x box_rows x kb_bytes and the swizzle of that row

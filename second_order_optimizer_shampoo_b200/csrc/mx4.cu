@@ -439,7 +439,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp == 0) {
     if (lane == 0) {
       // ---------------- TMA producer (both CTAs)
-      int kit = 0;
+      RingPos<STAGES> ring;
+      const uint32_t stages = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty);
+      const uint32_t fleader = mapa_shared(full0, 0);
       bool stop = false;
       for (int t = cl; t < ntiles && !stop; t += ncl) {
         const int b = t / per_b, r = t % per_b;
@@ -448,77 +450,74 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int nb0 = tn * BN + static_cast<int>(rank) * 128;
         const int za = b * p.rb_a + tm * 2 + static_cast<int>(rank);
         const int zb = b * p.rb_b + tn * 2;
-        for (int kb = 0; kb < KB; ++kb, ++kit) {
-          const int s = kit % STAGES;
-          if (kit >= STAGES &&
-              (*abort_flag || !mbar_wait(&empty[s], ((kit / STAGES) - 1) & 1, abort_flag))) {
-            *abort_flag = 1;
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!ring_wait(empty0 + ring.slot * 8, ring.parity ^ 1u, abort_flag)) {
             stop = true;
             break;
           }
-          uint8_t* sa = smem + s * STAGE_BYTES;
-          uint8_t* sf = sa + 2 * TILE_BYTES;
-          if (leader) mbar_arrive_expect_tx(&full[s], 2 * STAGE_BYTES);
-          const uint32_t fbar = mapa_shared(smem_u32(&full[s]), 0);
-          tma_load_3d_pair(sa, &tA, fbar, kb * 64, m0, b);  // codes move as 16-bit units
-          tma_load_3d_pair(sa + TILE_BYTES, &tB, fbar, kb * 64, nb0, b);
-          tma_load_3d_pair(sf, &tAs, fbar, 0, kb * 2, za);
-          tma_load_3d_pair(sf + 1024, &tBs, fbar, 0, kb * 2, zb);
-          tma_load_3d_pair(sf + 2048, &tBs, fbar, 0, kb * 2, zb + 1);
+          const uint32_t sa = stages + ring.slot * STAGE_BYTES, sf = sa + 2 * TILE_BYTES;
+          const uint32_t fbar = fleader + ring.slot * 8;
+          if (leader) mbar_expect_tx_u32(full0 + ring.slot * 8, 2 * STAGE_BYTES);
+          tma_3d_pair(sa, &tA, fbar, kb * 64, m0, b);  // codes move as 16-bit units
+          tma_3d_pair(sa + TILE_BYTES, &tB, fbar, kb * 64, nb0, b);
+          tma_3d_pair(sf, &tAs, fbar, 0, kb * 2, za);
+          tma_4d_pair(sf + 1024, &tBs, fbar, 0, kb * 2, zb, 0);
+          ring.advance();
         }
       }
       // a wait that gave up leaves copies in flight that no MMA waits for: let
       // them land (bounded) before the CTAs exit
       if (stop && leader) {
-        for (int k = kit > STAGES ? kit - STAGES : 0; k < kit; ++k)
-          mbar_wait(&full[k % STAGES], (k / STAGES) & 1);
+        for (int k = 0; k < STAGES; ++k, ring.advance())
+          mbar_wait(&full[ring.slot], ring.parity ^ 1u);
       }
     }
   } else if (warp == 1) {
     if (lane == 0 && leader) {
       // ---------------- MMA issuer (leader of the pair)
-      int kit = 0, it = 0;
+      RingPos<STAGES> ring;
+      const uint32_t full0 = smem_u32(full), acce0 = smem_u32(acce);
+      const uint64_t adesc = smem_desc(smem_u32(smem), 16, 1024u, 2u);
+      const uint64_t bdesc = smem_desc(smem_u32(smem) + TILE_BYTES, 16, 1024u, 2u);
+      const uint64_t sdesc = smem_desc(smem_u32(smem) + 2 * TILE_BYTES, 128, 128, 0);
+      uint32_t u = 0, pe = 1;  // accumulator; parity of acce's last use
+      uint32_t sf = 0;         // scale buffer
       bool stop = false;
       for (int t = cl; t < ntiles && !stop; t += ncl) {
-        for (int c0 = 0; c0 < KB && !stop; c0 += F32 ? CHUNK_KB : KB, ++it) {
+        for (int c0 = 0; c0 < KB && !stop; c0 += F32 ? CHUNK_KB : KB, u ^= 1u, pe ^= 1u) {
           const int c1 = F32 ? min(c0 + CHUNK_KB, KB) : KB;
-          const int u = it & 1;
-          if (it >= 1 && (*abort_flag || !mbar_wait(acce, (it - 1) & 1, abort_flag))) {
-            *abort_flag = 1;
+          if (!ring_wait(acce0, pe, abort_flag)) {
             stop = true;
             break;
           }
           tc_fence_after();
-          const uint32_t dacc = tmem + static_cast<uint32_t>(u * ACC1);
-          for (int kb = c0; kb < c1; ++kb, ++kit) {
-            const int s = kit % STAGES;
-            if (*abort_flag || !mbar_wait(&full[s], (kit / STAGES) & 1, abort_flag)) {
-              *abort_flag = 1;
+          const uint32_t dacc = tmem + u * ACC1;
+          for (int kb = c0; kb < c1; ++kb) {
+            if (!ring_wait(full0 + ring.slot * 8, ring.parity, abort_flag)) {
               stop = true;
               break;
             }
             tc_fence_after();
-            const uint32_t sa = smem_u32(smem + s * STAGE_BYTES), sb = sa + TILE_BYTES;
-            const uint32_t sf = sb + TILE_BYTES;
-            const uint32_t tsa = tmem + static_cast<uint32_t>(SF_COL + (kit & 1) * 24);
-            const uint32_t tsb = tsa + 8;
+            const uint64_t at = static_cast<uint64_t>(ring.slot) * (STAGE_BYTES >> 4);
+            const uint32_t tsa = tmem + SF_COL + sf * 24, tsb = tsa + 8;
+            sf ^= 1u;
             const int left = p.K - kb * MK;  // columns of this stage inside the matrix
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               if (k * 128 >= left) break;
-              tmem_cp_scales_pair(tsa + k * 4, smem_desc(sf + k * 512, 128, 128, 0));
-              tmem_cp_scales_pair(tsb + k * 8, smem_desc(sf + 1024 + k * 512, 128, 128, 0));
-              tmem_cp_scales_pair(tsb + k * 8 + 4, smem_desc(sf + 2048 + k * 512, 128, 128, 0));
+              tmem_cp_scales_pair(tsa + k * 4, sdesc + at + k * 32);
+              tmem_cp_scales_pair(tsb + k * 8, sdesc + at + 64 + k * 32);
+              tmem_cp_scales_pair(tsb + k * 8 + 4, sdesc + at + 128 + k * 32);
             }
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
               if (ks * 64 >= left) break;
-              mma_mxf4_pair(dacc, smem_desc(sa + ks * 32, 16, 1024u, 2u),
-                            smem_desc(sb + ks * 32, 16, 1024u, 2u),
+              mma_mxf4_pair(dacc, adesc + at + ks * 2, bdesc + at + ks * 2,
                             instr_desc_mxf4(256, BN, (ks & 1) * 2), tsa + (ks >> 1) * 4,
                             tsb + (ks >> 1) * 8, (kb > c0 || ks > 0) ? 1u : 0u);
             }
-            mma_commit_pair(&empty[s], 3);
+            mma_commit_pair(&empty[ring.slot], 3);
+            ring.advance();
           }
           mma_commit_pair(&accf[u], 3);
         }
@@ -707,7 +706,7 @@ cudaError_t mx4_gemm(const uint8_t* A, const uint8_t* As, const uint8_t* B, cons
   p.rb_a = static_cast<int>(ceil_div(M, 128));
   p.rb_b = static_cast<int>(ceil_div(N, 128));
   p.out = C;
-  const int kt = static_cast<int>(ceil_div(K, 128));
+  const int64_t kt = ceil_div(K, 128);
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n * batch;
   if (tiles > INT32_MAX / 2 || batch * p.rb_a > INT32_MAX || batch * p.rb_b > INT32_MAX)
     return cudaErrorInvalidValue;
@@ -717,8 +716,9 @@ cudaError_t mx4_gemm(const uint8_t* A, const uint8_t* As, const uint8_t* B, cons
       !tensor_map(&b, B, 2, u, N, batch, u, u * N, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !tensor_map(&as, As, 4, 128, kt, batch * p.rb_a, 128, 128 * kt, 128, 2,
                   CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      !tensor_map(&bs, Bs, 4, 128, kt, batch * p.rb_b, 128, 128 * kt, 128, 2,
-                  CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !tensor_map4(&bs, Bs, 4, {128, kt, batch * p.rb_b, 1},
+                   {128, 128 * kt, 128 * kt * batch * p.rb_b}, {128, 2, 2, 1},
+                   CU_TENSOR_MAP_SWIZZLE_NONE) ||
       !tensor_map(&o, C, f32 ? 4 : 2, N, M, batch, N, static_cast<int64_t>(M) * N, f32 ? 32 : 64, 32,
                   CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;

@@ -68,21 +68,65 @@ SHP_DEV bool mbar_wait(uint64_t* bar, uint32_t parity, const volatile int* abort
   return true;
 }
 
+// A position in a ring of N stages: the slot and the parity of its current use.
+// A producer waits with parity ^ 1, which a fresh barrier passes at once.
+// Counting instead of dividing a running index by N keeps the one-thread issue
+// loops short: their instructions, not the copies, set a ring's rate.
+template <int N>
+struct RingPos {
+  uint32_t slot = 0, parity = 0;
+  SHP_DEV void advance() {
+    if (++slot == N) {
+      slot = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
+// try_wait that may suspend the thread for up to about 16 us: a polling warp
+// takes issue slots and shared-memory cycles from the issuing threads beside it.
+SHP_DEV uint32_t mbar_try_wait_long(uint32_t addr, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(addr), "r"(parity), "r"(16384u)
+      : "memory");
+  return ok;
+}
+
+// Bounded wait by shared address; the abort flag is looked at only when the
+// phase is not complete yet, and set on giving up.
+SHP_DEV bool ring_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_try_wait_long(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait_long(bar, parity)) {
+    if (*abort_flag || clock64() - t0 > SHP_SPIN_LIMIT) {
+      *abort_flag = 1;
+      return false;
+    }
+  }
+  return true;
+}
+SHP_DEV void mbar_expect_tx_u32(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+
+// A whole warp waits; false for every lane if one lane's wait gave up, so that
+// the warp leaves its loop together.
+SHP_DEV bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, ring_wait(smem_u32(bar), parity, abort_flag));
+}
+
 // Limit of the wait a bounded-wait self-test points at a barrier nothing
 // completes (about 10 ms): long enough to be a real wait, short for a test.
 #define SHP_SELFTEST_LIMIT (20000000LL)
 
 SHP_DEV void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
-// A whole warp waits; false for every lane if one lane's wait gave up, so that
-// the warp leaves its loop together.
-SHP_DEV bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  const bool ok = *abort_flag == 0 && mbar_wait(bar, parity, abort_flag);
-  if (__all_sync(0xffffffffu, ok)) return true;
-  *abort_flag = 1;
-  return false;
 }
 
 // ----------------------------------------------------------------- TMA
@@ -209,6 +253,22 @@ SHP_DEV void tma_load_3d_pair(void* dst, const CUtensorMap* map, uint32_t mbar, 
       "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(mbar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+// The same with a shared address as destination.
+SHP_DEV void tma_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t mbar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(mbar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+SHP_DEV void tma_4d_pair(uint32_t dst, const CUtensorMap* map, uint32_t mbar, int x, int y, int z,
+                         int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(mbar), "r"(x), "r"(y), "r"(z), "r"(w)
       : "memory");
 }
 SHP_DEV void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {  // one warp in each CTA
