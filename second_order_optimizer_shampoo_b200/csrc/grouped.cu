@@ -107,10 +107,10 @@ struct RowWalk {
         const int lo = __shfl_sync(0xffffffffu, a, src), hi = __shfl_sync(0xffffffffu, b, src);
         const int tiles = (hi - lo + NT - 1) / NT;
         const int per = ((hi - lo + tiles - 1) / tiles + 15) & ~15;  // <= NT
-        x.e = e0 + src;
-        x.t0 = lo + r / tiles_n * per;
-        x.count = min(per, hi - x.t0);
-        x.n0 = r % tiles_n * 256;
+        x.e = uniform(e0 + src);
+        x.t0 = uniform(lo + r / tiles_n * per);
+        x.count = uniform(min(per, hi - x.t0));
+        x.n0 = uniform(r % tiles_n * 256);
         t += step;
         return true;
       }
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(RowsCfg<NT>::THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1) + 1;
   static_assert((2 * STAGES + 5) * 8 + 8 <= 512, "barriers");
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
@@ -196,16 +196,17 @@ __global__ void __launch_bounds__(RowsCfg<NT>::THREADS, 1)
   __syncthreads();
   cluster_sync();  // peer barriers initialised, both TMEM allocations done
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
 
   RowWalk<NT> walk(p.g, p.N, cl, ncl);
   RowTile x;
   if (warp == 0) {
     // ---------------- TMA producer (both CTAs): its 128 columns of W and its
     // half of the tile's rows, in boxes of 32
+    const uint32_t on = elect_one(), lead = on & (leader ? 1u : 0u);
     RingPos<STAGES> ring;
     const uint32_t stages = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty);
-    const uint32_t fleader = mapa_shared(full0, 0);
+    const uint32_t fleader = uniform(mapa_shared(full0, 0));
     bool stop = false;
     while (!stop && walk.next(x)) {
       const int n0 = x.n0 + static_cast<int>(rank) * 128;
@@ -215,81 +216,77 @@ __global__ void __launch_bounds__(RowsCfg<NT>::THREADS, 1)
       const bool small = half <= NT / 4;
       const int boxes = (half + 31) / 32;
       const uint32_t tx = 2 * (A_BYTES + (small ? boxes * 4096u : C::X_BYTES));
-      if (lane == 0) {
-        for (int k0 = 0; k0 < p.K; k0 += BK) {
-          if (!ring_wait(empty0 + ring.slot * 8, ring.parity ^ 1u, abort_flag)) {
-            stop = true;
-            break;
-          }
-          const uint32_t sw = stages + ring.slot * C::STAGE, sx = sw + A_BYTES;
-          const uint32_t fbar = fleader + ring.slot * 8;
-          if (leader) mbar_expect_tx_u32(full0 + ring.slot * 8, tx);
-          if (W_MN && p.w_chunks) {
-            tma_4d_pair(sw, &tW, fbar, 0, k0, n0 >> 6, x.e);
-          } else if (W_MN) {
-            tma_3d_pair(sw, &tW, fbar, n0, k0, x.e);
-            tma_3d_pair(sw + BK * 128, &tW, fbar, n0 + 64, k0, x.e);
-          } else {
-            tma_3d_pair(sw, &tW, fbar, k0, n0, x.e);
-          }
-          if (!small) {
-            tma_3d_pair(sx, &tX, fbar, k0, t0, 0);
-          } else {
-            for (int i = 0; i < boxes; ++i)
-              tma_3d_pair(sx + i * 4096, &tX32, fbar, k0, t0 + i * 32, 0);
-          }
-          ring.advance();
+      for (int k0 = 0; k0 < p.K; k0 += BK) {
+        if (!warp_wait(empty0 + ring.slot * 8, ring.parity ^ 1u, abort_flag)) {
+          stop = true;
+          break;
         }
+        const uint32_t sw = stages + ring.slot * C::STAGE, sx = sw + A_BYTES;
+        const uint32_t fbar = fleader + ring.slot * 8;
+        mbar_expect_tx_if(lead, full0 + ring.slot * 8, tx);
+        if (W_MN && p.w_chunks) {
+          tma_4d_pair_if(on, sw, &tW, fbar, 0, k0, n0 >> 6, x.e);
+        } else if (W_MN) {
+          tma_3d_pair_if(on, sw, &tW, fbar, n0, k0, x.e);
+          tma_3d_pair_if(on, sw + BK * 128, &tW, fbar, n0 + 64, k0, x.e);
+        } else {
+          tma_3d_pair_if(on, sw, &tW, fbar, k0, n0, x.e);
+        }
+        if (!small) {
+          tma_3d_pair_if(on, sx, &tX, fbar, k0, t0, 0);
+        } else {
+          for (int i = 0; i < boxes; ++i)
+            tma_3d_pair_if(on, sx + i * 4096, &tX32, fbar, k0, t0 + i * 32, 0);
+        }
+        ring.advance();
       }
-      stop = __shfl_sync(0xffffffffu, stop ? 1 : 0, 0) != 0;
     }
     // a wait that gave up leaves copies in flight that no MMA waits for: let
     // them land (bounded) before the CTAs exit
-    if (stop && leader && lane == 0) {
+    if (stop && leader) {
       for (int k = 0; k < STAGES; ++k, ring.advance()) mbar_wait(&full[ring.slot], ring.parity ^ 1u);
     }
   } else if (warp == 1) {
     if (leader) {
       // ---------------- MMA issuer (leader of the pair)
+      const uint32_t on = elect_one();
       RingPos<STAGES> ring;
       RingPos<2> au;  // accumulator
-      const uint32_t full0 = smem_u32(full), acce0 = smem_u32(acce);
+      const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
+      const uint32_t accf0 = smem_u32(accf), acce0 = smem_u32(acce);
       const uint64_t wdesc = W_MN ? smem_desc(smem_u32(smem), BK * 128, 1024u, 2u)
                                   : smem_desc(smem_u32(smem), 16, 1024u, 2u);
       const uint64_t xdesc = smem_desc(smem_u32(smem) + A_BYTES, 16, 1024u, 2u);
       constexpr uint64_t WSTEP = (W_MN ? 16 * 128 : 32) >> 4, XSTEP = 32 >> 4;
       bool stop = false;
       while (!stop && walk.next(x)) {
-        if (lane == 0) {
-          const uint32_t idesc = instr_desc(1u, W_MN, false, 256, (x.count + 15) & ~15);
-          for (int c0 = 0; c0 < KB && !stop; c0 += F32 ? CHUNK_KB : KB, au.advance()) {
-            const int c1 = F32 ? min(c0 + CHUNK_KB, KB) : KB;
-            if (!ring_wait(acce0 + au.slot * 8, au.parity ^ 1u, abort_flag)) {
+        const uint32_t idesc = instr_desc(1u, W_MN, false, 256, (x.count + 15) & ~15);
+        for (int c0 = 0; c0 < KB && !stop; c0 += F32 ? CHUNK_KB : KB, au.advance()) {
+          const int c1 = F32 ? min(c0 + CHUNK_KB, KB) : KB;
+          if (!warp_wait(acce0 + au.slot * 8, au.parity ^ 1u, abort_flag)) {
+            stop = true;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t dacc = tmem + au.slot * NT;
+          for (int kb = c0; kb < c1; ++kb) {
+            if (!warp_wait(full0 + ring.slot * 8, ring.parity, abort_flag)) {
               stop = true;
               break;
             }
             tc_fence_after();
-            const uint32_t dacc = tmem + au.slot * NT;
-            for (int kb = c0; kb < c1; ++kb) {
-              if (!ring_wait(full0 + ring.slot * 8, ring.parity, abort_flag)) {
-                stop = true;
-                break;
-              }
-              tc_fence_after();
-              const uint64_t at = static_cast<uint64_t>(ring.slot) * (C::STAGE >> 4);
+            const uint64_t at = static_cast<uint64_t>(ring.slot) * (C::STAGE >> 4);
 #pragma unroll
-              for (int ks = 0; ks < BK / 16; ++ks)
-                mma_f16_pair(dacc, wdesc + at + ks * WSTEP, xdesc + at + ks * XSTEP, idesc,
-                             (kb > c0 || ks > 0) ? 1u : 0u);
-              mma_commit_pair(&empty[ring.slot], 3);
-              ring.advance();
-            }
-            mma_commit_pair(&accf[au.slot], 3);
+            for (int ks = 0; ks < BK / 16; ++ks)
+              mma_f16_pair_if(on, dacc, wdesc + at + ks * WSTEP, xdesc + at + ks * XSTEP, idesc,
+                              (kb > c0 || ks > 0) ? 1u : 0u);
+            mma_commit_pair_if(on, empty0 + ring.slot * 8, 3);
+            ring.advance();
           }
+          mma_commit_pair_if(on, accf0 + au.slot * 8, 3);
         }
-        stop = __shfl_sync(0xffffffffu, stop ? 1 : 0, 0) != 0;
       }
-      if (lane == 0) mma_commit_pair(drain, 3);  // after every MMA issued above
+      mma_commit_pair_if(on, smem_u32(drain), 3);  // after every MMA issued above
     }
   } else {
     // ---------------- epilogue warps (both CTAs, each on its TMEM rows): warp
@@ -308,7 +305,7 @@ __global__ void __launch_bounds__(RowsCfg<NT>::THREADS, 1)
         for (int j = 0; j < NC * 32; ++j) acc[j] = 0.f;
         for (int c0 = 0; c0 < KB; c0 += CHUNK_KB, ++it) {
           const int u = it & 1;
-          if (!warp_wait(&accf[u], (it >> 1) & 1, abort_flag)) {
+          if (!warp_wait(smem_u32(&accf[u]), (it >> 1) & 1, abort_flag)) {
             stop = true;
             break;
           }
@@ -339,7 +336,7 @@ __global__ void __launch_bounds__(RowsCfg<NT>::THREADS, 1)
         }
       } else {
         const int u = it & 1;
-        if (!warp_wait(&accf[u], (it >> 1) & 1, abort_flag)) break;
+        if (!warp_wait(smem_u32(&accf[u]), (it >> 1) & 1, abort_flag)) break;
         ++it;
         tc_fence_after();
         // lane l stores columns nb + (l & ~1), + 1 of the even (odd) rows
@@ -413,6 +410,8 @@ struct Walk {
     const int r = t % per_e;
     int lo, hi;
     p.g.range(x.e, lo, hi);
+    lo = uniform(lo);
+    hi = uniform(hi);
     x.m0 = r / tiles_n * 256;
     x.n0 = r % tiles_n * BN;
     x.k0 = lo;
@@ -447,7 +446,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(drain + 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1) + 1;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
@@ -471,110 +470,106 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   cluster_sync();  // peer barriers initialised, both TMEM allocations done
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
 
   Walk walk(p, cl, ncl);
   Tile x;
   if (warp == 0) {
     // ---------------- TMA producer (both CTAs)
+    const uint32_t on = elect_one(), lead = on & (leader ? 1u : 0u);
     RingPos<STAGES> ring;
     const uint32_t stages = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty);
-    const uint32_t fleader = mapa_shared(full0, 0);
+    const uint32_t tail0 = smem_u32(tailb), fleader = uniform(mapa_shared(full0, 0));
     bool stop = false;
     while (!stop && walk.next(x)) {
       const int m0 = x.m0 + static_cast<int>(rank) * 128;
       const int nb0 = x.n0 + static_cast<int>(rank) * 128;
       const int whole = x.kb - (x.tail != 0 ? 1 : 0);  // stages without a tail
-      if (lane == 0) {
-        for (int kb = 0; kb < x.kb; ++kb) {
-          if (!ring_wait(empty0 + ring.slot * 8, ring.parity ^ 1u, abort_flag)) {
-            stop = true;
-            break;
-          }
-          const uint32_t sa = stages + ring.slot * STAGE_BYTES, sb = sa + A_BYTES;
-          const int k0 = x.k0 + kb * BK;
-          if (kb >= whole) {
-            // partial stage: this CTA's halves, for the clearing warp
-            uint64_t* bar = &tailb[ring.slot];
-            uint8_t* st = smem + ring.slot * STAGE_BYTES;
-            mbar_arrive_expect_tx(bar, STAGE_BYTES);
-            for (int i = 0; i < 2; ++i) {
-              tma_load_3d(st + i * BK * 128, &tA, bar, m0 + i * 64, k0, 0);
-              tma_load_3d(st + A_BYTES + i * BK * 128, &tB, bar, nb0 + i * 64, k0, 0);
-            }
-          } else {
-            const uint32_t fbar = fleader + ring.slot * 8;
-            if (leader) mbar_expect_tx_u32(full0 + ring.slot * 8, 2 * STAGE_BYTES);
-            if (p.chunks) {
-              tma_4d_pair(sa, &tA2, fbar, 0, k0, m0 >> 6, 0);
-              tma_4d_pair(sb, &tB2, fbar, 0, k0, nb0 >> 6, 0);
-            } else {
-              for (int i = 0; i < 2; ++i) {
-                tma_3d_pair(sa + i * BK * 128, &tA, fbar, m0 + i * 64, k0, 0);
-                tma_3d_pair(sb + i * BK * 128, &tB, fbar, nb0 + i * 64, k0, 0);
-              }
-            }
-          }
-          ring.advance();
+      for (int kb = 0; kb < x.kb; ++kb) {
+        if (!warp_wait(empty0 + ring.slot * 8, ring.parity ^ 1u, abort_flag)) {
+          stop = true;
+          break;
         }
+        const uint32_t sa = stages + ring.slot * STAGE_BYTES, sb = sa + A_BYTES;
+        const int k0 = x.k0 + kb * BK;
+        if (kb >= whole) {
+          // partial stage: this CTA's halves, for the clearing warp
+          const uint32_t bar = tail0 + ring.slot * 8;
+          mbar_expect_tx_if(on, bar, STAGE_BYTES);
+          for (int i = 0; i < 2; ++i) {
+            tma_3d_if(on, sa + i * BK * 128, &tA, bar, m0 + i * 64, k0, 0);
+            tma_3d_if(on, sb + i * BK * 128, &tB, bar, nb0 + i * 64, k0, 0);
+          }
+        } else {
+          const uint32_t fbar = fleader + ring.slot * 8;
+          mbar_expect_tx_if(lead, full0 + ring.slot * 8, 2 * STAGE_BYTES);
+          if (p.chunks) {
+            tma_4d_pair_if(on, sa, &tA2, fbar, 0, k0, m0 >> 6, 0);
+            tma_4d_pair_if(on, sb, &tB2, fbar, 0, k0, nb0 >> 6, 0);
+          } else {
+            for (int i = 0; i < 2; ++i) {
+              tma_3d_pair_if(on, sa + i * BK * 128, &tA, fbar, m0 + i * 64, k0, 0);
+              tma_3d_pair_if(on, sb + i * BK * 128, &tB, fbar, nb0 + i * 64, k0, 0);
+            }
+          }
+        }
+        ring.advance();
       }
-      stop = __shfl_sync(0xffffffffu, stop ? 1 : 0, 0) != 0;
     }
     // a wait that gave up leaves copies in flight that no MMA waits for: let
     // them land (bounded) before the CTAs exit
-    if (stop && leader && lane == 0) {
+    if (stop && leader) {
       for (int k = 0; k < STAGES; ++k, ring.advance()) mbar_wait(&full[ring.slot], ring.parity ^ 1u);
     }
   } else if (warp == 1) {
     if (leader) {
       // ---------------- MMA issuer (leader of the pair)
       const uint32_t idesc = instr_desc(1u, true, true, 256, BN);
+      const uint32_t on = elect_one();
       RingPos<STAGES> ring;
       RingPos<2> au;  // accumulator
-      const uint32_t full0 = smem_u32(full), acce0 = smem_u32(acce);
+      const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
+      const uint32_t accf0 = smem_u32(accf), acce0 = smem_u32(acce);
       const uint64_t adesc = smem_desc(smem_u32(smem), BK * 128, 1024u, 2u);
       const uint64_t bdesc = smem_desc(smem_u32(smem) + A_BYTES, BK * 128, 1024u, 2u);
       constexpr uint64_t KSTEP = 16 * 128 >> 4;
       bool stop = false;
       while (!stop && walk.next(x)) {
-        if (lane == 0) {
-          const int whole = x.kb - (x.tail != 0 ? 1 : 0);
-          for (int c0 = 0; c0 < x.kb && !stop; c0 += CHUNK_KB, au.advance()) {
-            const int c1 = min(c0 + CHUNK_KB, x.kb);
-            if (!ring_wait(acce0 + au.slot * 8, au.parity ^ 1u, abort_flag)) {
+        const int whole = x.kb - (x.tail != 0 ? 1 : 0);
+        for (int c0 = 0; c0 < x.kb && !stop; c0 += CHUNK_KB, au.advance()) {
+          const int c1 = min(c0 + CHUNK_KB, x.kb);
+          if (!warp_wait(acce0 + au.slot * 8, au.parity ^ 1u, abort_flag)) {
+            stop = true;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t dacc = tmem + au.slot * BN;
+          for (int kb = c0; kb < c1; ++kb) {
+            if (!warp_wait(full0 + ring.slot * 8, ring.parity, abort_flag)) {
               stop = true;
               break;
             }
-            tc_fence_after();
-            const uint32_t dacc = tmem + au.slot * BN;
-            for (int kb = c0; kb < c1; ++kb) {
-              if (!ring_wait(full0 + ring.slot * 8, ring.parity, abort_flag)) {
-                stop = true;
-                break;
-              }
-              const uint64_t at = static_cast<uint64_t>(ring.slot) * (STAGE_BYTES >> 4);
-              if (kb < whole) {
-                tc_fence_after();
+            const uint64_t at = static_cast<uint64_t>(ring.slot) * (STAGE_BYTES >> 4);
+            if (kb < whole) {
+              tc_fence_after();
 #pragma unroll
-                for (int ks = 0; ks < BK / 16; ++ks)
-                  mma_f16_pair(dacc, adesc + at + ks * KSTEP, bdesc + at + ks * KSTEP, idesc,
-                               (kb > c0 || ks > 0) ? 1u : 0u);
-              } else {
-                fence_cluster();  // the peer's half was cleared by its own warp
-                tc_fence_after();
-                for (int ks = 0; ks < (x.tail + 15) / 16; ++ks)
-                  mma_f16_pair(dacc, adesc + at + ks * KSTEP, bdesc + at + ks * KSTEP, idesc,
-                               (kb > c0 || ks > 0) ? 1u : 0u);
-              }
-              mma_commit_pair(&empty[ring.slot], 3);
-              ring.advance();
+              for (int ks = 0; ks < BK / 16; ++ks)
+                mma_f16_pair_if(on, dacc, adesc + at + ks * KSTEP, bdesc + at + ks * KSTEP, idesc,
+                                (kb > c0 || ks > 0) ? 1u : 0u);
+            } else {
+              fence_cluster();  // the peer's half was cleared by its own warp
+              tc_fence_after();
+              for (int ks = 0; ks < (x.tail + 15) / 16; ++ks)
+                mma_f16_pair_if(on, dacc, adesc + at + ks * KSTEP, bdesc + at + ks * KSTEP, idesc,
+                                (kb > c0 || ks > 0) ? 1u : 0u);
             }
-            mma_commit_pair(&accf[au.slot], 3);
+            mma_commit_pair_if(on, empty0 + ring.slot * 8, 3);
+            ring.advance();
           }
+          mma_commit_pair_if(on, accf0 + au.slot * 8, 3);
         }
-        stop = __shfl_sync(0xffffffffu, stop ? 1 : 0, 0) != 0;
       }
-      if (lane == 0) mma_commit_pair(drain, 3);  // after every MMA issued above
+      mma_commit_pair_if(on, smem_u32(drain), 3);  // after every MMA issued above
     }
   } else if (warp < 2 + EPI_WARPS) {
     // ---------------- epilogue warps (both CTAs, each on its TMEM rows)
@@ -592,7 +587,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int nc = (x.kb + CHUNK_KB - 1) / CHUNK_KB;
         for (int c = 0; c < nc; ++c, ++it) {
           const int u = it & 1;
-          if (!warp_wait(&accf[u], (it >> 1) & 1, abort_flag)) {
+          if (!warp_wait(smem_u32(&accf[u]), (it >> 1) & 1, abort_flag)) {
             stop = true;
             break;
           }
@@ -643,7 +638,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       kit += x.kb;
       if (x.tail == 0) continue;
       const int s = (kit - 1) % STAGES;
-      if (!warp_wait(&tailb[s], (par >> s) & 1, abort_flag)) break;
+      if (!warp_wait(smem_u32(&tailb[s]), (par >> s) & 1, abort_flag)) break;
       uint8_t* st = smem + s * STAGE_BYTES;
       const int r1 = (x.tail + 15) / 16 * 16;
       // four 64-column chunks (two of A, two of B) of 64 rows of 128 bytes
@@ -659,7 +654,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!leader) {
         if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&clearb[s]), 0));
       } else {
-        if (!warp_wait(&clearb[s], (par >> s) & 1, abort_flag)) break;
+        if (!warp_wait(smem_u32(&clearb[s]), (par >> s) & 1, abort_flag)) break;
         fence_cluster();
         if (lane == 0) mbar_arrive(&full[s]);
       }

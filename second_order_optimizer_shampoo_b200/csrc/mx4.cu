@@ -355,19 +355,23 @@ static_assert(ACC1 + BN == SF_COL && SF_COL + 2 * 24 <= 512, "tensor memory");
 // One scale tile (32 rows of 16 bytes) to four columns of tensor memory,
 // repeated in all four lane quarters, in both CTAs of the pair (each from its
 // own shared memory).
-SHP_DEV void tmem_cp_scales_pair(uint32_t taddr, uint64_t sdesc) {
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
-               : "memory");
+SHP_DEV void tmem_cp_scales_pair_if(uint32_t on, uint32_t taddr, uint64_t sdesc) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
+      "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%1], %2;\n\t}" ::"r"(on),
+      "r"(taddr), "l"(sdesc)
+      : "memory");
 }
 
-SHP_DEV void mma_mxf4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                           uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+SHP_DEV void mma_mxf4_pair_if(uint32_t on, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                              uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X"
-      " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate));
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 q, %0, 0;\n\t"
+      "setp.ne.b32 p, %7, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X"
+      " [%1], %2, %3, %4, [%5], [%6], p;\n\t}" ::"r"(on),
+      "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate));
 }
 
 // Instruction descriptor of the block-scaled kinds: E2M1 operands (format 1),
@@ -411,7 +415,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(drain + 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1) + 1;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
@@ -434,49 +438,50 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   cluster_sync();  // peer barriers initialised, both TMEM allocations done
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ---------------- TMA producer (both CTAs)
-      RingPos<STAGES> ring;
-      const uint32_t stages = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty);
-      const uint32_t fleader = mapa_shared(full0, 0);
-      bool stop = false;
-      for (int t = cl; t < ntiles && !stop; t += ncl) {
-        const int b = t / per_b, r = t % per_b;
-        const int tm = r / p.tiles_n, tn = r % p.tiles_n;
-        const int m0 = tm * 256 + static_cast<int>(rank) * 128;
-        const int nb0 = tn * BN + static_cast<int>(rank) * 128;
-        const int za = b * p.rb_a + tm * 2 + static_cast<int>(rank);
-        const int zb = b * p.rb_b + tn * 2;
-        for (int kb = 0; kb < KB; ++kb) {
-          if (!ring_wait(empty0 + ring.slot * 8, ring.parity ^ 1u, abort_flag)) {
-            stop = true;
-            break;
-          }
-          const uint32_t sa = stages + ring.slot * STAGE_BYTES, sf = sa + 2 * TILE_BYTES;
-          const uint32_t fbar = fleader + ring.slot * 8;
-          if (leader) mbar_expect_tx_u32(full0 + ring.slot * 8, 2 * STAGE_BYTES);
-          tma_3d_pair(sa, &tA, fbar, kb * 64, m0, b);  // codes move as 16-bit units
-          tma_3d_pair(sa + TILE_BYTES, &tB, fbar, kb * 64, nb0, b);
-          tma_3d_pair(sf, &tAs, fbar, 0, kb * 2, za);
-          tma_4d_pair(sf + 1024, &tBs, fbar, 0, kb * 2, zb, 0);
-          ring.advance();
+    // ---------------- TMA producer (both CTAs)
+    const uint32_t on = elect_one(), lead = on & (leader ? 1u : 0u);
+    RingPos<STAGES> ring;
+    const uint32_t stages = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty);
+    const uint32_t fleader = uniform(mapa_shared(full0, 0));
+    bool stop = false;
+    for (int t = cl; t < ntiles && !stop; t += ncl) {
+      const int b = t / per_b, r = t % per_b;
+      const int tm = r / p.tiles_n, tn = r % p.tiles_n;
+      const int m0 = tm * 256 + static_cast<int>(rank) * 128;
+      const int nb0 = tn * BN + static_cast<int>(rank) * 128;
+      const int za = b * p.rb_a + tm * 2 + static_cast<int>(rank);
+      const int zb = b * p.rb_b + tn * 2;
+      for (int kb = 0; kb < KB; ++kb) {
+        if (!warp_wait(empty0 + ring.slot * 8, ring.parity ^ 1u, abort_flag)) {
+          stop = true;
+          break;
         }
-      }
-      // a wait that gave up leaves copies in flight that no MMA waits for: let
-      // them land (bounded) before the CTAs exit
-      if (stop && leader) {
-        for (int k = 0; k < STAGES; ++k, ring.advance())
-          mbar_wait(&full[ring.slot], ring.parity ^ 1u);
+        const uint32_t sa = stages + ring.slot * STAGE_BYTES, sf = sa + 2 * TILE_BYTES;
+        const uint32_t fbar = fleader + ring.slot * 8;
+        mbar_expect_tx_if(lead, full0 + ring.slot * 8, 2 * STAGE_BYTES);
+        tma_3d_pair_if(on, sa, &tA, fbar, kb * 64, m0, b);  // codes move as 16-bit units
+        tma_3d_pair_if(on, sa + TILE_BYTES, &tB, fbar, kb * 64, nb0, b);
+        tma_3d_pair_if(on, sf, &tAs, fbar, 0, kb * 2, za);
+        tma_4d_pair_if(on, sf + 1024, &tBs, fbar, 0, kb * 2, zb, 0);
+        ring.advance();
       }
     }
+    // a wait that gave up leaves copies in flight that no MMA waits for: let
+    // them land (bounded) before the CTAs exit
+    if (stop && leader) {
+      for (int k = 0; k < STAGES; ++k, ring.advance())
+        mbar_wait(&full[ring.slot], ring.parity ^ 1u);
+    }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    if (leader) {
       // ---------------- MMA issuer (leader of the pair)
+      const uint32_t on = elect_one();
       RingPos<STAGES> ring;
-      const uint32_t full0 = smem_u32(full), acce0 = smem_u32(acce);
+      const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
+      const uint32_t accf0 = smem_u32(accf), acce0 = smem_u32(acce);
       const uint64_t adesc = smem_desc(smem_u32(smem), 16, 1024u, 2u);
       const uint64_t bdesc = smem_desc(smem_u32(smem) + TILE_BYTES, 16, 1024u, 2u);
       const uint64_t sdesc = smem_desc(smem_u32(smem) + 2 * TILE_BYTES, 128, 128, 0);
@@ -486,14 +491,14 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int t = cl; t < ntiles && !stop; t += ncl) {
         for (int c0 = 0; c0 < KB && !stop; c0 += F32 ? CHUNK_KB : KB, u ^= 1u, pe ^= 1u) {
           const int c1 = F32 ? min(c0 + CHUNK_KB, KB) : KB;
-          if (!ring_wait(acce0, pe, abort_flag)) {
+          if (!warp_wait(acce0, pe, abort_flag)) {
             stop = true;
             break;
           }
           tc_fence_after();
           const uint32_t dacc = tmem + u * ACC1;
           for (int kb = c0; kb < c1; ++kb) {
-            if (!ring_wait(full0 + ring.slot * 8, ring.parity, abort_flag)) {
+            if (!warp_wait(full0 + ring.slot * 8, ring.parity, abort_flag)) {
               stop = true;
               break;
             }
@@ -505,24 +510,24 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               if (k * 128 >= left) break;
-              tmem_cp_scales_pair(tsa + k * 4, sdesc + at + k * 32);
-              tmem_cp_scales_pair(tsb + k * 8, sdesc + at + 64 + k * 32);
-              tmem_cp_scales_pair(tsb + k * 8 + 4, sdesc + at + 128 + k * 32);
+              tmem_cp_scales_pair_if(on, tsa + k * 4, sdesc + at + k * 32);
+              tmem_cp_scales_pair_if(on, tsb + k * 8, sdesc + at + 64 + k * 32);
+              tmem_cp_scales_pair_if(on, tsb + k * 8 + 4, sdesc + at + 128 + k * 32);
             }
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
               if (ks * 64 >= left) break;
-              mma_mxf4_pair(dacc, adesc + at + ks * 2, bdesc + at + ks * 2,
-                            instr_desc_mxf4(256, BN, (ks & 1) * 2), tsa + (ks >> 1) * 4,
-                            tsb + (ks >> 1) * 8, (kb > c0 || ks > 0) ? 1u : 0u);
+              mma_mxf4_pair_if(on, dacc, adesc + at + ks * 2, bdesc + at + ks * 2,
+                               instr_desc_mxf4(256, BN, (ks & 1) * 2), tsa + (ks >> 1) * 4,
+                               tsb + (ks >> 1) * 8, (kb > c0 || ks > 0) ? 1u : 0u);
             }
-            mma_commit_pair(&empty[ring.slot], 3);
+            mma_commit_pair_if(on, empty0 + ring.slot * 8, 3);
             ring.advance();
           }
-          mma_commit_pair(&accf[u], 3);
+          mma_commit_pair_if(on, accf0 + u * 8, 3);
         }
       }
-      mma_commit_pair(drain, 3);  // after every MMA issued above
+      mma_commit_pair_if(on, smem_u32(drain), 3);  // after every MMA issued above
     }
   } else {
     // ---------------- epilogue warps 2..9 (both CTAs, each on its TMEM rows)
@@ -544,7 +549,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int j = 0; j < 128; ++j) acc[j] = 0.f;
         for (int c0 = 0; c0 < KB; c0 += CHUNK_KB, ++it) {
           const int u = it & 1;
-          if (!warp_wait(&accf[u], (it >> 1) & 1, abort_flag)) {
+          if (!warp_wait(smem_u32(&accf[u]), (it >> 1) & 1, abort_flag)) {
             stop = true;
             break;
           }
@@ -585,7 +590,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       } else {
         const int u = it & 1;
-        if (!warp_wait(&accf[u], (it >> 1) & 1, abort_flag)) break;
+        if (!warp_wait(smem_u32(&accf[u]), (it >> 1) & 1, abort_flag)) break;
         ++it;
         tc_fence_after();
 #pragma unroll

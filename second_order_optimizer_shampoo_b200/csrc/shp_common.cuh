@@ -110,15 +110,10 @@ SHP_DEV bool ring_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) 
   }
   return true;
 }
-SHP_DEV void mbar_expect_tx_u32(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-               : "memory");
-}
-
 // A whole warp waits; false for every lane if one lane's wait gave up, so that
 // the warp leaves its loop together.
-SHP_DEV bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  return __all_sync(0xffffffffu, ring_wait(smem_u32(bar), parity, abort_flag));
+SHP_DEV bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, ring_wait(bar, parity, abort_flag));
 }
 
 // Limit of the wait a bounded-wait self-test points at a barrier nothing
@@ -255,22 +250,6 @@ SHP_DEV void tma_load_3d_pair(void* dst, const CUtensorMap* map, uint32_t mbar, 
       "l"(reinterpret_cast<uint64_t>(map)), "r"(mbar), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
-// The same with a shared address as destination.
-SHP_DEV void tma_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t mbar, int x, int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(mbar), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-SHP_DEV void tma_4d_pair(uint32_t dst, const CUtensorMap* map, uint32_t mbar, int x, int y, int z,
-                         int w) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(mbar), "r"(x), "r"(y), "r"(z), "r"(w)
-      : "memory");
-}
 SHP_DEV void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {  // one warp in each CTA
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                    smem_u32(dst_smem)),
@@ -308,6 +287,78 @@ SHP_DEV void mma_commit_pair(uint64_t* bar, uint16_t mask) {
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
       " [%0], %1;" ::"r"(smem_u32(bar)),
       "h"(mask)
+      : "memory");
+}
+
+// ----------------------------------------------------- warp-uniform issue
+// The copy and MMA instructions take their operands from uniform registers.
+// Inside an `if (lane == 0)` block the compiler keeps everything in per-thread
+// registers and moves each operand across before each instruction: 70 to 90
+// clocks per instruction, measured, which bounds kernels whose stages need
+// many.  So an issuing warp runs its loop as a whole on warp-uniform values,
+// and one elected lane (`on`) executes the instruction under a predicate.
+SHP_DEV uint32_t elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r;
+}
+// A value every lane holds, as one the compiler knows to be warp-uniform.
+SHP_DEV int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+SHP_DEV uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+SHP_DEV void mbar_expect_tx_if(uint32_t on, uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%1], %2;\n\t}" ::"r"(on),
+      "r"(bar), "r"(bytes)
+      : "memory");
+}
+SHP_DEV void tma_3d_if(uint32_t on, uint32_t dst, const CUtensorMap* map, uint32_t mbar, int x,
+                       int y, int z) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
+      "@q cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%1], [%2, {%4, %5, %6}], [%3];\n\t}" ::"r"(on),
+      "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(mbar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+SHP_DEV void tma_3d_pair_if(uint32_t on, uint32_t dst, const CUtensorMap* map, uint32_t mbar,
+                            int x, int y, int z) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
+      "@q cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%1], [%2, {%4, %5, %6}], [%3];\n\t}" ::"r"(on),
+      "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(mbar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+SHP_DEV void tma_4d_pair_if(uint32_t on, uint32_t dst, const CUtensorMap* map, uint32_t mbar,
+                            int x, int y, int z, int w) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
+      "@q cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%1], [%2, {%4, %5, %6, %7}], [%3];\n\t}" ::"r"(on),
+      "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(mbar), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+SHP_DEV void mma_f16_pair_if(uint32_t on, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                             uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 q, %0, 0;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%1], %2, %3, %4, p;\n\t}" ::"r"(on),
+      "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+SHP_DEV void mma_commit_pair_if(uint32_t on, uint32_t bar, uint16_t mask) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%1], %2;\n\t}" ::"r"(on),
+      "r"(bar), "h"(mask)
       : "memory");
 }
 
