@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(RowsCfg<NT>::THREADS, 1)
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acce[u]), 0));
+          if (lane == 0) mbar_arrive_relaxed(mapa_shared(smem_u32(&acce[u]), 0));
         }
         if (stop) break;
         if (nb + lane < p.N) {
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(RowsCfg<NT>::THREADS, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acce[u]), 0));
+        if (lane == 0) mbar_arrive_relaxed(mapa_shared(smem_u32(&acce[u]), 0));
       }
     }
   }
@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acce[u]), 0));
+          if (lane == 0) mbar_arrive_relaxed(mapa_shared(smem_u32(&acce[u]), 0));
         }
         if (stop) break;
         if (p.accumulate && nc == 0) continue;  // an empty group leaves G as it is

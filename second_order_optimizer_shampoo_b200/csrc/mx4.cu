@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (g == 1) {
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(acce), 0));
+              if (lane == 0) mbar_arrive_relaxed(mapa_shared(smem_u32(acce), 0));
             }
           }
         }
@@ -596,21 +596,19 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           const int part = (g ^ h) * 64;
-          uint32_t w[32];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float v[32];
-            tmem_ld32(trow + static_cast<uint32_t>(u * ACC1 + h * 128 + part + k * 32), v);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-              w[16 * k + j] = *reinterpret_cast<const uint32_t*>(&x);
-            }
-          }
+          uint32_t w[64];
+          tmem_ld64_async(trow + static_cast<uint32_t>(u * ACC1 + h * 128 + part), w);
+          tmem_ld_wait();
           if (g == 0) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(acce), 0));
+            if (lane == 0) mbar_arrive_relaxed(mapa_shared(smem_u32(acce), 0));
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const __nv_bfloat162 x =
+                __floats2bfloat162_rn(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+            w[j] = *reinterpret_cast<const uint32_t*>(&x);
           }
           if (row0 < p.M && n0 + part < p.N) {
             if (lane == 0) bulk_wait_read_all();
