@@ -158,6 +158,10 @@ SHP_DEV void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y,
 SHP_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // This thread's committed bulk stores have finished reading shared memory.
 SHP_DEV void bulk_wait_read_all() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+// All but the latest of this thread's bulk groups have finished reading.
+SHP_DEV void bulk_wait_read_but_one() {
+  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+}
 // This thread's committed bulk stores are complete.
 SHP_DEV void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // Orders this thread's generic-proxy shared-memory accesses before later
@@ -392,6 +396,96 @@ SHP_DEV void mma_commit_pair_if(uint32_t on, uint32_t bar, uint16_t mask) {
       "r"(bar), "h"(mask)
       : "memory");
 }
+
+// ------------------------------------------------- dynamic tile scheduling
+// A grid of one cluster (CTA pair) per tile, of which only those that fit run:
+// a running pair that wants another tile cancels the launch of a waiting one
+// and does that one's work (cluster launch control).  The hardware hands tiles
+// out as pairs become free, with no counter in memory to clear or to share
+// between launches.  A scheduler warp of the leader CTA asks, and passes the
+// tile's number to the roles of both CTAs through two slots.
+struct TileSlots {
+  uint64_t full[2];   // per CTA: the slot holds a tile (or -1: no more)
+  uint64_t empty[2];  // leader: every consumer of both CTAs has read it
+  uint64_t asked;     // leader: the answer has arrived
+  alignas(16) uint4 answer;
+  int tile[2];
+};
+
+// Asks for another cluster; 16 bytes arrive in `answer`, counted on `bar`.
+SHP_DEV void try_cancel_cluster(uint32_t answer, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128"
+      " [%0], [%1];" ::"r"(answer),
+      "r"(bar)
+      : "memory");
+}
+// First CTA index (x) of the cancelled cluster, or -1 if none was left.
+SHP_DEV int cancelled_cta(uint32_t answer) {
+  int x = -1;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\t.reg .b32 y, z;\n\t"
+      "ld.shared.b128 a, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, _}, a;\n\t}"
+      : "+r"(x)
+      : "r"(answer)
+      : "memory");
+  return x;
+}
+// Stores v in a CTA's shared memory (cluster address), 4 bytes counted on its
+// barrier, on which this thread also arrives.
+SHP_DEV void slot_store(uint32_t addr, int v, uint32_t bar) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], 4;" ::"r"(bar)
+               : "memory");
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr),
+               "r"(v), "r"(bar)
+               : "memory");
+}
+
+SHP_DEV void tile_slots_init(TileSlots* ts, int consumers) {
+  for (int i = 0; i < 2; ++i) {
+    mbar_init(&ts->full[i], 1);
+    mbar_init(&ts->empty[i], consumers);
+  }
+  mbar_init(&ts->asked, 1);
+}
+
+// The scheduler, one thread of the leader.  Every wait is bounded.
+SHP_DEV void schedule_tiles(TileSlots* ts, volatile int* abort_flag) {
+  RingPos<2> at;
+  uint32_t asked = 0;
+  for (;;) {
+    if (!ring_wait(smem_u32(&ts->empty[at.slot]), at.parity ^ 1u, abort_flag)) return;
+    mbar_arrive_expect_tx(&ts->asked, 16);
+    try_cancel_cluster(smem_u32(&ts->answer), smem_u32(&ts->asked));
+    if (!ring_wait(smem_u32(&ts->asked), asked, abort_flag)) return;
+    asked ^= 1u;
+    const int cta = cancelled_cta(smem_u32(&ts->answer));
+    fence_proxy_async_smem();  // read before the next answer is written
+    for (uint32_t r = 0; r < 2; ++r)
+      slot_store(mapa_shared(smem_u32(&ts->tile[at.slot]), r), cta < 0 ? -1 : cta / 2,
+                 mapa_shared(smem_u32(&ts->full[at.slot]), r));
+    if (cta < 0) return;
+    at.advance();
+  }
+}
+
+// A consumer warp's view: next() gives the following tile's number to every
+// lane, or -1 when there is none left (or a wait gave up).
+struct TileFeed {
+  TileSlots* ts;
+  volatile int* abort_flag;
+  RingPos<2> at;
+  SHP_DEV int next() {
+    if (!warp_wait(smem_u32(&ts->full[at.slot]), at.parity, abort_flag)) return -1;
+    const int t = uniform(*const_cast<volatile int*>(&ts->tile[at.slot]));
+    if ((threadIdx.x & 31) == 0)
+      mbar_arrive_relaxed(mapa_shared(smem_u32(&ts->empty[at.slot]), 0));
+    at.advance();
+    return t;
+  }
+};
 
 // Shared-memory matrix descriptor (sm_100 layout version 1).
 //   start address, leading-dimension byte offset and stride-dimension byte

@@ -302,25 +302,38 @@ def shp_matmul(Amat, B, prec="tf32", a_trans=False, b_trans=False, A_lo=None, B_
 
 
 def _ready(*ts):
-    """Checks that the tensors are contiguous and on the current CUDA device;
-    returns the handle of its current stream."""
-    for t in ts:
-        if t is not None and not (t.is_cuda and t.is_contiguous()):
-            _dev(t)
+    """Checks that the tensors (None is skipped) are contiguous and on the
+    current CUDA device; returns the handle of its current stream."""
+    if not ts[0].is_cuda:
+        _dev(*ts)
     dev = torch.cuda.current_device()
     for t in ts:
-        if t is not None and t.get_device() != dev:
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            _dev(t)
             raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
     return torch.cuda.current_stream(dev).cuda_stream
 
 
-def _a(t):
-    return None if t is None else t.data_ptr()
-
-
 def _want(name, t, dtype, shape):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+
+
+_STORAGE = {torch.bfloat16: A.SHP_BF16, torch.float32: A.SHP_TF32}
+
+
+def _storage(dtype):
+    if dtype not in _STORAGE:
+        raise ValueError(f"bfloat16 or float32, not {dtype}")
+    return _STORAGE[dtype]
+
+
+def _result(out, shape, dtype, device):
+    """`out`, checked, or a new tensor; and its storage code."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device), _storage(dtype)
+    _want("out", out, out.dtype, shape)
+    return out, _storage(out.dtype)
 
 
 def shp_grouped_matmul(X, offsets, W, w_trans=False, out=None, dtype=torch.bfloat16):
@@ -333,17 +346,17 @@ def shp_grouped_matmul(X, offsets, W, w_trans=False, out=None, dtype=torch.bfloa
     a new [T, N] tensor of `dtype` (bf16 or float32) whose rows outside every
     group are uninitialised; in `out` those rows are left as they were."""
     st = _ready(X, offsets, W, out)
-    if X.dim() != 2 or W.dim() != 3 or offsets.dim() != 1:
-        raise ValueError("X is [T, K], W [groups, K, N] and offsets [groups + 1]")
+    if X.dim() != 2 or W.dim() != 3:
+        raise ValueError("X is [T, K] and W [groups, K, N]")
     T, K = X.shape
-    groups, N = W.shape[0], W.shape[1] if w_trans else W.shape[2]
+    groups, N = W.shape[0], W.shape[1 if w_trans else 2]
     _want("X", X, torch.bfloat16, (T, K))
     _want("W", W, torch.bfloat16, (groups, N, K) if w_trans else (groups, K, N))
     _want("offsets", offsets, torch.int64, (groups + 1,))
-    out = torch.empty(T, N, dtype=dtype, device=X.device) if out is None else out
-    _want("out", out, out.dtype, (T, N))
-    _check(A.lib().shp_grouped_matmul(_a(X), _a(offsets), _a(W), int(bool(w_trans)), _a(out),
-                                      _storage(out.dtype), T, K, N, groups, st), "shp_grouped_matmul")
+    out, storage = _result(out, (T, N), dtype, X.device)
+    _check(A.lib().shp_grouped_matmul(X.data_ptr(), offsets.data_ptr(), W.data_ptr(),
+                                      1 if w_trans else 0, out.data_ptr(), storage, T, K, N,
+                                      groups, st), "shp_grouped_matmul")
     return out
 
 
@@ -364,25 +377,26 @@ def shp_grouped_wgrad(Amat, B, offsets, out=None, accumulate=False):
     _want("A", Amat, torch.bfloat16, (T, m))
     _want("B", B, torch.bfloat16, (T, n))
     _want("offsets", offsets, torch.int64, (groups + 1,))
-    out = torch.empty(groups, m, n, dtype=torch.float32, device=B.device) if out is None else out
-    _want("out", out, torch.float32, (groups, m, n))
-    _check(A.lib().shp_grouped_wgrad(_a(Amat), _a(B), _a(offsets), _a(out), T, m, n, groups,
-                                     int(bool(accumulate)), st), "shp_grouped_wgrad")
+    if out is None:
+        out = torch.empty((groups, m, n), dtype=torch.float32, device=B.device)
+    else:
+        _want("out", out, torch.float32, (groups, m, n))
+    _check(A.lib().shp_grouped_wgrad(Amat.data_ptr(), B.data_ptr(), offsets.data_ptr(),
+                                     out.data_ptr(), T, m, n, groups, 1 if accumulate else 0, st),
+           "shp_grouped_wgrad")
     return out
 
 
-_STORAGE = {torch.bfloat16: A.SHP_BF16, torch.float32: A.SHP_TF32}
-
-
-def _storage(dtype):
-    if dtype not in _STORAGE:
-        raise ValueError(f"bfloat16 or float32, not {dtype}")
-    return _STORAGE[dtype]
-
-
 def _mx4_shapes(batch, rows, cols):
+    """Shapes of the codes and of the scale tiles."""
     return ((batch, rows, (cols + 31) // 32 * 16),
             (batch, (rows + 127) // 128, (cols + 127) // 128, 512))
+
+
+def _mx4_new(batch, rows, cols, device):
+    q, s = _mx4_shapes(batch, rows, cols)
+    return (torch.empty(q, dtype=torch.uint8, device=device),
+            torch.empty(s, dtype=torch.uint8, device=device))
 
 
 def shp_mx4_quantize(X, along="cols"):
@@ -395,14 +409,18 @@ def shp_mx4_quantize(X, along="cols"):
     st = _ready(X)
     if along not in ("cols", "rows", "both") or X.dim() not in (2, 3):
         raise ValueError("X is [batch, rows, cols] or [rows, cols]; along is cols, rows or both")
-    rows, cols = X.shape[-2], X.shape[-1]
+    rows, cols = X.shape[-2:]
     batch = X.shape[0] if X.dim() == 3 else 1
-    new = lambda shapes: [torch.empty(s, dtype=torch.uint8, device=X.device) for s in shapes]  # noqa: E731
-    q = new(_mx4_shapes(batch, rows, cols)) if along != "rows" else [None, None]
-    qt = new(_mx4_shapes(batch, cols, rows)) if along != "cols" else [None, None]
-    _check(A.lib().shp_mx4_quantize(_a(X), _storage(X.dtype), rows, cols, batch, _a(q[0]), _a(q[1]),
-                                    _a(qt[0]), _a(qt[1]), st), "shp_mx4_quantize")
-    return tuple(t for t in q + qt if t is not None)
+    storage = _storage(X.dtype)
+    res = () if along == "rows" else _mx4_new(batch, rows, cols, X.device)
+    if along != "cols":
+        res += _mx4_new(batch, cols, rows, X.device)
+    ptrs = [t.data_ptr() for t in res]
+    if along != "both":
+        ptrs = ptrs + [None, None] if along == "cols" else [None, None] + ptrs
+    _check(A.lib().shp_mx4_quantize(X.data_ptr(), storage, rows, cols, batch, *ptrs, st),
+           "shp_mx4_quantize")
+    return res
 
 
 def shp_mx4_dequantize(Q, S, cols, dtype=torch.float32, out=None):
@@ -410,13 +428,13 @@ def shp_mx4_dequantize(Q, S, cols, dtype=torch.float32, out=None):
     st = _ready(Q, S, out)
     if Q.dim() != 3:
         raise ValueError("Q is [batch, rows, Cp / 2]")
-    batch, rows = Q.shape[0], Q.shape[1]
-    for name, t, shape in zip(("Q", "S"), (Q, S), _mx4_shapes(batch, rows, cols)):
-        _want(name, t, torch.uint8, shape)
-    out = torch.empty(batch, rows, cols, dtype=dtype, device=Q.device) if out is None else out
-    _want("out", out, out.dtype, (batch, rows, cols))
-    _check(A.lib().shp_mx4_dequantize(_a(Q), _a(S), rows, cols, batch, _a(out),
-                                      _storage(out.dtype), st), "shp_mx4_dequantize")
+    batch, rows = Q.shape[:2]
+    q, s = _mx4_shapes(batch, rows, cols)
+    _want("Q", Q, torch.uint8, q)
+    _want("S", S, torch.uint8, s)
+    out, storage = _result(out, (batch, rows, cols), dtype, Q.device)
+    _check(A.lib().shp_mx4_dequantize(Q.data_ptr(), S.data_ptr(), rows, cols, batch,
+                                      out.data_ptr(), storage, st), "shp_mx4_dequantize")
     return out
 
 
@@ -427,15 +445,17 @@ def shp_mx4_matmul(Amat, A_scales, B, B_scales, dtype=torch.bfloat16, out=None):
     st = _ready(Amat, A_scales, B, B_scales, out)
     if Amat.dim() != 3 or B.dim() != 3:
         raise ValueError("A is [batch, M, K / 2] and B [batch, N, K / 2]")
-    batch, M, K = Amat.shape[0], Amat.shape[1], Amat.shape[2] * 2
-    N = B.shape[1]
-    for name, t, shape in zip(("A", "A_scales", "B", "B_scales"), (Amat, A_scales, B, B_scales),
-                              _mx4_shapes(batch, M, K) + _mx4_shapes(batch, N, K)):
-        _want(name, t, torch.uint8, shape)
-    out = torch.empty(batch, M, N, dtype=dtype, device=B.device) if out is None else out
-    _want("out", out, out.dtype, (batch, M, N))
-    _check(A.lib().shp_mx4_matmul(_a(Amat), _a(A_scales), _a(B), _a(B_scales), _a(out),
-                                  _storage(out.dtype), M, N, K, batch, st),
+    batch, M, half = Amat.shape
+    N, K = B.shape[1], 2 * half
+    q, s = _mx4_shapes(batch, M, K)
+    _want("A", Amat, torch.uint8, q)
+    _want("A_scales", A_scales, torch.uint8, s)
+    q, s = _mx4_shapes(batch, N, K)
+    _want("B", B, torch.uint8, q)
+    _want("B_scales", B_scales, torch.uint8, s)
+    out, storage = _result(out, (batch, M, N), dtype, B.device)
+    _check(A.lib().shp_mx4_matmul(Amat.data_ptr(), A_scales.data_ptr(), B.data_ptr(),
+                                  B_scales.data_ptr(), out.data_ptr(), storage, M, N, K, batch, st),
            "shp_mx4_matmul")
     return out
 
