@@ -397,9 +397,13 @@ struct WgradParams {
 };
 
 // One tile: group e, tile (m0, n0), kb stages from row k0; `tail` valid rows in
-// the last stage (0: all 64).
+// the last stage (0: all 64).  Clearing a partial stage and handing it over
+// takes longer than a stage's MMAs, so it is loaded TAIL_EARLY stages ahead of
+// its turn (`tail_at`: its place in the order of loading; -1: none) and used
+// last: 64 groups of 250 rows, 1024 x 1024: 77 -> 72 us (of 256 rows: 64 us).
+constexpr int TAIL_EARLY = STAGES - 2;  // the stages behind it still fit in the ring
 struct Tile {
-  int e, m0, n0, k0, kb, tail;
+  int e, m0, n0, k0, kb, tail, tail_at;
 };
 
 // A role's walk over its pair's tiles.
@@ -429,6 +433,7 @@ struct Walk {
     x.k0 = lo;
     x.kb = (hi - lo + BK - 1) / BK;
     x.tail = (hi - lo) % BK;
+    x.tail_at = x.tail == 0 ? -1 : max(0, x.kb - 1 - TAIL_EARLY);
     return true;
   }
 };
@@ -515,21 +520,21 @@ __global__ void __launch_bounds__(THREADS, 1)
     while (!stop && walk.next(x)) {
       const int m0 = x.m0 + static_cast<int>(rank) * 128;
       const int nb0 = x.n0 + static_cast<int>(rank) * 128;
-      const int whole = x.kb - (x.tail != 0 ? 1 : 0);  // stages without a tail
-      for (int kb = 0; kb < x.kb; ++kb) {
+      int k0 = x.k0;
+      for (int l = 0; l < x.kb; ++l) {
         if (!warp_wait(empty0 + ring.slot * 8, ring.parity ^ 1u, abort_flag)) {
           stop = true;
           break;
         }
         const uint32_t sa = stages + ring.slot * STAGE_BYTES, sb = sa + A_BYTES;
-        const int k0 = x.k0 + kb * BK;
-        if (kb >= whole) {
+        if (l == x.tail_at) {
           // partial stage: this CTA's halves, for the clearing warp
           const uint32_t bar = tail0 + ring.slot * 8;
+          const int kt = x.k0 + (x.kb - 1) * BK;
           mbar_expect_tx_if(on, bar, STAGE_BYTES);
           for (int i = 0; i < 2; ++i) {
-            tma_3d_if(on, sa + i * BK * 128, &tA, bar, m0 + i * 64, k0, 0);
-            tma_3d_if(on, sb + i * BK * 128, &tB, bar, nb0 + i * 64, k0, 0);
+            tma_3d_if(on, sa + i * BK * 128, &tA, bar, m0 + i * 64, kt, 0);
+            tma_3d_if(on, sb + i * BK * 128, &tB, bar, nb0 + i * 64, kt, 0);
           }
         } else {
           const uint32_t fbar = fleader + ring.slot * 8;
@@ -543,6 +548,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               tma_3d_pair_if(on, sb + i * BK * 128, &tB, fbar, nb0 + i * 64, k0, 0);
             }
           }
+          k0 += BK;
         }
         ring.advance();
       }
@@ -566,38 +572,44 @@ __global__ void __launch_bounds__(THREADS, 1)
       constexpr uint64_t KSTEP = 16 * 128 >> 4;
       bool stop = false;
       while (!stop && walk.next(x)) {
-        const int whole = x.kb - (x.tail != 0 ? 1 : 0);
-        for (int c0 = 0; c0 < x.kb && !stop; c0 += CHUNK_KB, au.advance()) {
-          const int c1 = min(c0 + CHUNK_KB, x.kb);
-          if (!warp_wait(acce0 + au.slot * 8, au.parity ^ 1u, abort_flag)) {
+        int l = 0;                 // place in the order of loading
+        RingPos<STAGES> tail = ring;  // where the partial stage is
+        for (int kb = 0; kb < x.kb; ++kb) {
+          const int c = kb % CHUNK_KB;
+          if (c == 0 && !warp_wait(acce0 + au.slot * 8, au.parity ^ 1u, abort_flag)) {
+            stop = true;
+            break;
+          }
+          if (l++ == x.tail_at) {
+            tail = ring;
+            ring.advance();
+            ++l;
+          }
+          const bool last = kb == x.kb - 1, partial = last && x.tail != 0;
+          const RingPos<STAGES> at = partial ? tail : ring;
+          if (!warp_wait(full0 + at.slot * 8, at.parity, abort_flag)) {
             stop = true;
             break;
           }
           tc_fence_after();
           const uint32_t dacc = tmem + au.slot * BN;
-          for (int kb = c0; kb < c1; ++kb) {
-            if (!warp_wait(full0 + ring.slot * 8, ring.parity, abort_flag)) {
-              stop = true;
-              break;
-            }
-            const uint64_t at = static_cast<uint64_t>(ring.slot) * (STAGE_BYTES >> 4);
-            if (kb < whole) {
-              tc_fence_after();
-#pragma unroll
-              for (int ks = 0; ks < BK / 16; ++ks)
-                mma_f16_pair_if(on, dacc, adesc + at + ks * KSTEP, bdesc + at + ks * KSTEP, idesc,
-                                (kb > c0 || ks > 0) ? 1u : 0u);
-            } else {
-              fence_cluster();  // the peer's half was cleared by its own warp
-              tc_fence_after();
-              for (int ks = 0; ks < (x.tail + 15) / 16; ++ks)
-                mma_f16_pair_if(on, dacc, adesc + at + ks * KSTEP, bdesc + at + ks * KSTEP, idesc,
-                                (kb > c0 || ks > 0) ? 1u : 0u);
-            }
-            mma_commit_pair_if(on, empty0 + ring.slot * 8, 3);
+          const uint64_t da = static_cast<uint64_t>(at.slot) * (STAGE_BYTES >> 4);
+          if (!partial) {
             ring.advance();
+#pragma unroll
+            for (int ks = 0; ks < BK / 16; ++ks)
+              mma_f16_pair_if(on, dacc, adesc + da + ks * KSTEP, bdesc + da + ks * KSTEP, idesc,
+                              (c > 0 || ks > 0) ? 1u : 0u);
+          } else {
+            for (int ks = 0; ks < (x.tail + 15) / 16; ++ks)
+              mma_f16_pair_if(on, dacc, adesc + da + ks * KSTEP, bdesc + da + ks * KSTEP, idesc,
+                              (c > 0 || ks > 0) ? 1u : 0u);
           }
-          mma_commit_pair_if(on, accf0 + au.slot * 8, 3);
+          mma_commit_pair_if(on, empty0 + at.slot * 8, 3);
+          if (last || c == CHUNK_KB - 1) {
+            mma_commit_pair_if(on, accf0 + au.slot * 8, 3);
+            au.advance();
+          }
         }
       }
       mma_commit_pair_if(on, smem_u32(drain), 3);  // after every MMA issued above
@@ -672,9 +684,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     int kit = 0;
     uint32_t par = 0;  // phase of each stage's tailb and clearb
     while (walk.next(x)) {
-      kit += x.kb;
+      const int s = (kit + max(x.tail_at, 0)) % STAGES;
+      kit = (kit + x.kb) % STAGES;
       if (x.tail == 0) continue;
-      const int s = (kit - 1) % STAGES;
       if (!warp_wait(smem_u32(&tailb[s]), (par >> s) & 1, abort_flag)) break;
       uint8_t* st = smem + s * STAGE_BYTES;
       const int r1 = (x.tail + 15) / 16 * 16;
