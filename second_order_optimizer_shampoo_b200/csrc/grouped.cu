@@ -39,10 +39,6 @@ constexpr int BK = 64;                // contraction elements per stage: 128-byt
 constexpr int A_BYTES = 128 * 128;    // per CTA and stage: 128 rows (columns) of A
 constexpr int CHUNK_KB = 8;  // stages per fp32 chunk: sums of 512 products inside the tensor core
 constexpr int EPI_WARPS = 8;
-#ifndef NT_SMALL
-#define NT_SMALL 48
-#define NT_MID 128
-#endif
 
 SHP_DEV void tma_reduce_add_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
   asm volatile(
@@ -380,12 +376,12 @@ __global__ void __launch_bounds__(RowsCfg<NT>::THREADS, 1)
 // pair has 1 % more stages than the mean, in a fixed rotation 10 %.
 
 constexpr int STAGE_BYTES = 2 * A_BYTES;
-constexpr int STAGES = 5;
+constexpr int STAGES = 6;
 constexpr int BN = 256;
 constexpr int THREADS = 32 * (2 + EPI_WARPS + 2);
-constexpr int EPI_BOX = 4096;  // a 32 x 32 store box; two per epilogue warp
+constexpr int EPI_BOX = 4096;  // one warp's 32 x 32 store box
 constexpr int SORT_MAX = 256;  // groups that are put in order (each thread compares all)
-constexpr int GSMEM = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * 2 * EPI_BOX + 320 +
+constexpr int GSMEM = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * EPI_BOX + 320 +
                       static_cast<int>(sizeof(TileSlots)) + SORT_MAX * 2;
 static_assert(GSMEM <= 232448, "weight-gradient kernel exceeds shared memory");
 
@@ -451,7 +447,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* boxes = smem + STAGES * STAGE_BYTES;
-  TileSlots* slots = reinterpret_cast<TileSlots*>(boxes + EPI_WARPS * 2 * EPI_BOX);
+  TileSlots* slots = reinterpret_cast<TileSlots*>(boxes + EPI_WARPS * EPI_BOX);
   uint64_t* full = reinterpret_cast<uint64_t*>(slots + 1);
   uint64_t* empty = full + STAGES;
   uint64_t* accf = empty + STAGES;
@@ -617,8 +613,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else if (warp < 2 + EPI_WARPS) {
     // ---------------- epilogue warps (both CTAs, each on its TMEM rows)
     const int q = warp & 3, h = (warp - 2) >> 2;
-    uint8_t* box = boxes + (warp - 2) * 2 * EPI_BOX;
-    uint32_t turn = 0;  // the warp's two boxes alternate from store to store
+    uint8_t* box = boxes + (warp - 2) * EPI_BOX;
     const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * 128u;
     int it = 0;
     bool stop = false;
@@ -654,22 +649,20 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int g = 0; g < 4; ++g) {
           const int cb = c0 + g * 32;
           if (cb >= p.N) continue;
-          uint8_t* bx = box + turn * EPI_BOX;
-          turn ^= 1u;
-          if (lane == 0) bulk_wait_read_but_one();  // the last store from this box has read it
+          if (lane == 0) bulk_wait_read_all();  // the last store has read the box
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<float4*>(bx + sw128_off(lane, i)) =
+            *reinterpret_cast<float4*>(box + sw128_off(lane, i)) =
                 make_float4(acc[g * 32 + 4 * i], acc[g * 32 + 4 * i + 1], acc[g * 32 + 4 * i + 2],
                             acc[g * 32 + 4 * i + 3]);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
             if (p.accumulate)
-              tma_reduce_add_3d(&tO, bx, cb, row0, x.e);
+              tma_reduce_add_3d(&tO, box, cb, row0, x.e);
             else
-              tma_store_3d(&tO, bx, cb, row0, x.e);
+              tma_store_3d(&tO, box, cb, row0, x.e);
             bulk_commit();
           }
         }
@@ -764,6 +757,33 @@ cudaError_t dispatch_rows(const void* X, const CUtensorMap& w, bool w_mn, bool f
              : launch_rows<NT, false, false>(w, x, x32, p, T, st);
 }
 
+// Rows per tile.  The host knows the mean size of a group only, so it counts as
+// if all were equal: rounds of tiles over the SM pairs, times a tile's cost,
+// which grows with its rows beyond streaming W (a tile of 256 rows takes 1.6
+// times one of 16, measured).  Equal counts: with several rounds the larger
+// tile (fewer reads of W where groups differ: 8192 skewed rows over 64 blocks
+// of 1024 x 4096, 106 us against 116 with 128 and 145 with 64), in one round
+// the smaller (16 blocks of 4096 x 1024 with 16 rows each: 29 us against 32).
+int rows_per_tile(int64_t T, int64_t N, int64_t groups) {
+  const int64_t pairs = 74, tn = (N + 255) / 256;
+  const int64_t used = groups < T ? groups : T, mean = (T + used - 1) / used;
+  int best = 0;
+  double best_cost = 0;
+  int64_t best_rounds = 0;
+  for (int nt = 64; nt <= 256; nt *= 2) {
+    const int64_t per_group = (mean + nt - 1) / nt;
+    const int64_t rounds = (used * per_group * tn + pairs - 1) / pairs;
+    const double rows = static_cast<double>(mean) / static_cast<double>(per_group);
+    const double cost = static_cast<double>(rounds) * (1.0 + rows / 340.0);
+    if (best == 0 || cost < best_cost || (cost == best_cost && best_rounds > 1)) {
+      best = nt;
+      best_cost = cost;
+      best_rounds = rounds;
+    }
+  }
+  return best;
+}
+
 }  // namespace
 
 cudaError_t grouped_rows(const void* X, const int64_t* offsets, const void* W, bool w_trans,
@@ -787,10 +807,11 @@ cudaError_t grouped_rows(const void* X, const int64_t* offsets, const void* W, b
     ok = tensor_map(&w, W, 2, N, K, groups, N, kn, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B);
   }
   if (!ok) return cudaErrorInvalidValue;
-  const int64_t mean = T / groups;
-  if (mean <= NT_SMALL) return dispatch_rows<64>(X, w, !w_trans, f32, p, T, st);
-  if (mean <= NT_MID) return dispatch_rows<128>(X, w, !w_trans, f32, p, T, st);
-  return dispatch_rows<256>(X, w, !w_trans, f32, p, T, st);
+  switch (rows_per_tile(T, N, groups)) {
+    case 64: return dispatch_rows<64>(X, w, !w_trans, f32, p, T, st);
+    case 128: return dispatch_rows<128>(X, w, !w_trans, f32, p, T, st);
+    default: return dispatch_rows<256>(X, w, !w_trans, f32, p, T, st);
+  }
 }
 
 cudaError_t grouped_wgrad(const void* A, const void* B, const int64_t* offsets, float* G, int T,

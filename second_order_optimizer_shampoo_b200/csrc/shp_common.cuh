@@ -158,10 +158,6 @@ SHP_DEV void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y,
 SHP_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // This thread's committed bulk stores have finished reading shared memory.
 SHP_DEV void bulk_wait_read_all() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-// All but the latest of this thread's bulk groups have finished reading.
-SHP_DEV void bulk_wait_read_but_one() {
-  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-}
 // This thread's committed bulk stores are complete.
 SHP_DEV void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // Orders this thread's generic-proxy shared-memory accesses before later
