@@ -65,31 +65,81 @@ struct Groups {
   }
 };
 
+constexpr int SORT_MAX = 256;  // groups that are put in order (each thread compares all)
+
+// order[i] = the group of the i-th largest size (ties by number).  Called by all
+// threads of a block of at least SORT_MAX; `len` is scratch in shared memory.
+SHP_DEV void sort_groups(const Groups& g, uint16_t* order, int* len) {
+  const int e = static_cast<int>(threadIdx.x);
+  if (e < g.n) {
+    int lo, hi;
+    g.range(e, lo, hi);
+    len[e] = hi - lo;
+  }
+  __syncthreads();
+  if (e < g.n) {
+    int rank = 0;
+    for (int j = 0; j < g.n; ++j) rank += len[j] > len[e] || (len[j] == len[e] && j < e);
+    order[rank] = static_cast<uint16_t>(e);
+  }
+}
+
 // A tile of the rows product: `count` rows from row t0 in group e, weight
 // columns from n0.
 struct RowTile {
   int e, t0, count, n0;
 };
 
-// Walks the tiles of all groups in order, every role of the kernel the same
-// sequence.  A group of len rows has ceil(len / NT) row tiles of equal size (up
-// to the MMA's granule of 16), each with every column tile.  next() is called
-// by whole warps and looks at 32 groups per step.
+// A role's walk over its pair's tiles: its own, then, in a grid of more tiles
+// than pairs, the ones the scheduler passes on.  Tiles are numbered over the
+// groups in order (by falling size where sorted); a group of len rows has
+// ceil(len / NT) row tiles of equal size (up to the MMA's granule of 16), each
+// with every column tile.  next() is called by whole warps and looks at 32
+// groups per step.
 template <int NT>
 struct RowWalk {
   const Groups g;
-  const int tiles_n, step;
-  int t;
+  const uint16_t* order;  // null: the groups in their own order
+  const bool dynamic;
+  const int tiles_n;
+  TileFeed feed;
+  bool first = true;
   int e0 = 0;    // first group of the window
   int base = 0;  // tiles before the window
-  SHP_DEV RowWalk(const Groups& groups, int N, int first, int stride)
-      : g(groups), tiles_n((N + 255) / 256), step(stride), t(first) {}
+  SHP_DEV RowWalk(const Groups& groups, int N, const uint16_t* o, bool dyn, TileSlots* ts,
+                  volatile int* abort_flag)
+      : g(groups), order(o), dynamic(dyn), tiles_n((N + 255) / 256), feed{ts, abort_flag} {}
+  // Group number, rows and tiles of the lane's group of the window.
+  SHP_DEV int window(int lane, int& a, int& b, int& e) const {
+    a = b = 0;
+    e = e0 + lane;
+    if (e < g.n) {
+      if (order != nullptr) e = order[e];
+      g.range(e, a, b);
+    }
+    return (b - a + NT - 1) / NT * tiles_n;
+  }
+  SHP_DEV int total() {  // all tiles (whole warp; leaves the walk at its start)
+    int sum = 0;
+    for (e0 = 0; e0 < g.n; e0 += 32) {
+      int a, b, e;
+      sum += window(threadIdx.x & 31, a, b, e);
+    }
+    e0 = 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
+  }
   SHP_DEV bool next(RowTile& x) {
+    if (!first && !dynamic) return false;
+    const int t = first ? static_cast<int>(blockIdx.x) / 2 : feed.next();
+    first = false;
+    if (t < 0) return false;
+    if (t < base) e0 = base = 0;
     const int lane = threadIdx.x & 31;
     while (e0 < g.n) {
-      int a = 0, b = 0;
-      if (e0 + lane < g.n) g.range(e0 + lane, a, b);
-      const int cnt = (b - a + NT - 1) / NT * tiles_n;
+      int a, b, e;
+      const int cnt = window(lane, a, b, e);
       int inc = cnt;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -103,17 +153,16 @@ struct RowWalk {
         const int lo = __shfl_sync(0xffffffffu, a, src), hi = __shfl_sync(0xffffffffu, b, src);
         const int tiles = (hi - lo + NT - 1) / NT;
         const int per = ((hi - lo + tiles - 1) / tiles + 15) & ~15;  // <= NT
-        x.e = uniform(e0 + src);
+        x.e = uniform(__shfl_sync(0xffffffffu, e, src));
         x.t0 = uniform(lo + r / tiles_n * per);
         x.count = uniform(min(per, hi - x.t0));
         x.n0 = uniform(r % tiles_n * 256);
-        t += step;
         return true;
       }
       base += __shfl_sync(0xffffffffu, inc, 31);
       e0 += 32;
     }
-    return false;
+    return false;  // a number beyond the last tile
   }
 };
 
@@ -134,6 +183,7 @@ struct RowsParams {
   Groups g;
   int N, K;
   int w_chunks;  // W [K][N] is mapped as 64-column chunks: both of a CTA in one box
+  int dynamic;   // more tiles than pairs: they are handed out, the largest groups' first
   void* out;
 };
 
@@ -141,9 +191,10 @@ template <int NT>
 struct RowsCfg {
   static constexpr int X_BYTES = NT / 2 * 128;
   static constexpr int STAGE = A_BYTES + X_BYTES;
-  static constexpr int STAGES = (232448 - 1024 - 512) / STAGE;
-  static constexpr int SMEM = 1024 + STAGES * STAGE + 512;
-  static constexpr int THREADS = 32 * (2 + EPI_WARPS);
+  static constexpr int TAIL = 320 + static_cast<int>(sizeof(TileSlots)) + SORT_MAX * 2;
+  static constexpr int STAGES = (232448 - 1024 - TAIL) / STAGE;
+  static constexpr int SMEM = 1024 + STAGES * STAGE + TAIL;
+  static constexpr int THREADS = 32 * (2 + EPI_WARPS + 1);
 };
 
 template <int NT, bool W_MN, bool F32>
@@ -155,20 +206,22 @@ __global__ void __launch_bounds__(RowsCfg<NT>::THREADS, 1)
   constexpr int STAGES = C::STAGES;
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
-  const int ncl = static_cast<int>(gridDim.x) / 2, cl = static_cast<int>(blockIdx.x) / 2;
   const int KB = (p.K + BK - 1) / BK;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * C::STAGE);
+  TileSlots* slots = reinterpret_cast<TileSlots*>(smem + STAGES * C::STAGE);
+  uint64_t* full = reinterpret_cast<uint64_t*>(slots + 1);
   uint64_t* empty = full + STAGES;
   uint64_t* accf = empty + STAGES;
   uint64_t* acce = accf + 2;
   uint64_t* drain = acce + 2;  // all MMAs of this pair complete
   volatile int* abort_flag = reinterpret_cast<volatile int*>(drain + 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1) + 1;
-  static_assert((2 * STAGES + 5) * 8 + 8 <= 512, "barriers");
+  uint16_t* order = reinterpret_cast<uint16_t*>(drain + 2);
+  static_assert((2 * STAGES + 5) * 8 + 8 <= 320, "barriers");
+  const bool sorted = p.dynamic && p.g.n <= SORT_MAX;
 
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -181,6 +234,8 @@ __global__ void __launch_bounds__(RowsCfg<NT>::THREADS, 1)
       mbar_init(&acce[u], 2 * EPI_WARPS);
     }
     mbar_init(drain, 1);
+    // consumers: producer and epilogue warps of both CTAs, MMA warp
+    tile_slots_init(slots, 2 * (EPI_WARPS + 1) + 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tW);
@@ -188,13 +243,17 @@ __global__ void __launch_bounds__(RowsCfg<NT>::THREADS, 1)
     tma_prefetch_desc(&tX32);
   }
   if (warp == 1) tmem_alloc_pair(tmem_slot, 2 * NT);
+  if (sorted) {
+    sort_groups(p.g, order, reinterpret_cast<int*>(smem));
+    fence_proxy_async_smem();  // before the copies that reuse the space
+  }
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // peer barriers initialised, both TMEM allocations done
   tc_fence_after();
   const uint32_t tmem = uniform(*tmem_slot);
 
-  RowWalk<NT> walk(p.g, p.N, cl, ncl);
+  RowWalk<NT> walk(p.g, p.N, sorted ? order : nullptr, p.dynamic != 0, slots, abort_flag);
   RowTile x;
   if (warp == 0) {
     // ---------------- TMA producer (both CTAs): its 128 columns of W and its
@@ -283,6 +342,13 @@ __global__ void __launch_bounds__(RowsCfg<NT>::THREADS, 1)
         }
       }
       mma_commit_pair_if(on, smem_u32(drain), 3);  // after every MMA issued above
+    }
+  } else if (warp == 2 + EPI_WARPS) {
+    // ---------------- scheduler (leader)
+    if (leader && p.dynamic) {
+      const int total = uniform(walk.total());
+      if (lane == 0 && static_cast<int>(blockIdx.x) / 2 < total)
+        schedule_tiles(slots, total, abort_flag);
     }
   } else {
     // ---------------- epilogue warps (both CTAs, each on its TMEM rows): warp
@@ -380,7 +446,6 @@ constexpr int STAGES = 6;
 constexpr int BN = 256;
 constexpr int THREADS = 32 * (2 + EPI_WARPS + 2);
 constexpr int EPI_BOX = 4096;  // one warp's 32 x 32 store box
-constexpr int SORT_MAX = 256;  // groups that are put in order (each thread compares all)
 constexpr int GSMEM = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * EPI_BOX + 320 +
                       static_cast<int>(sizeof(TileSlots)) + SORT_MAX * 2;
 static_assert(GSMEM <= 232448, "weight-gradient kernel exceeds shared memory");
@@ -389,7 +454,8 @@ struct WgradParams {
   Groups g;
   int M, N;
   int accumulate;
-  int chunks;  // tA2, tB2 bring both 64-column chunks of a CTA in one box
+  int chunks;   // tA2, tB2 bring both 64-column chunks of a CTA in one box
+  int dynamic;  // more tiles than pairs: they are handed out
 };
 
 // One tile: group e, tile (m0, n0), kb stages from row k0; `tail` valid rows in
@@ -405,7 +471,7 @@ struct Tile {
 // A role's walk over its pair's tiles.
 struct Walk {
   const WgradParams& p;
-  const uint16_t* order;  // groups by falling size
+  const uint16_t* order;  // groups by falling size; null: in their own order
   TileFeed feed;
   int t, tiles_n, per_e;
   bool first = true;
@@ -415,11 +481,12 @@ struct Walk {
     per_e = tiles_n * ((q.M + 255) / 256);
   }
   SHP_DEV bool next(Tile& x) {
+    if (!first && !p.dynamic) return false;
     if (!first) t = feed.next();
     first = false;
     if (t < 0) return false;
     const int i = t / per_e, r = t % per_e;
-    x.e = p.g.n <= SORT_MAX ? uniform(static_cast<int>(order[i])) : i;
+    x.e = order != nullptr ? uniform(static_cast<int>(order[i])) : i;
     int lo, hi;
     p.g.range(x.e, lo, hi);
     lo = uniform(lo);
@@ -458,6 +525,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(drain + 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1) + 1;
   uint16_t* order = reinterpret_cast<uint16_t*>(drain + 2);
+  const bool sorted = p.dynamic && p.g.n <= SORT_MAX;
 
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -481,21 +549,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     tma_prefetch_desc(&tO);
   }
   if (warp == 1) tmem_alloc_pair(tmem_slot, 2 * BN);
-  if (p.g.n <= SORT_MAX) {
-    // rank of every group by size (ties by number), the sizes in the stages' space
-    int* len = reinterpret_cast<int*>(smem);
-    const int e = static_cast<int>(threadIdx.x);
-    if (e < p.g.n) {
-      int lo, hi;
-      p.g.range(e, lo, hi);
-      len[e] = hi - lo;
-    }
-    __syncthreads();
-    if (e < p.g.n) {
-      int rank_e = 0;
-      for (int j = 0; j < p.g.n; ++j) rank_e += len[j] > len[e] || (len[j] == len[e] && j < e);
-      order[rank_e] = static_cast<uint16_t>(e);
-    }
+  if (sorted) {
+    sort_groups(p.g, order, reinterpret_cast<int*>(smem));
     fence_proxy_async_smem();  // before the copies that reuse the space
   }
   tc_fence_before();
@@ -504,7 +559,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = uniform(*tmem_slot);
 
-  Walk walk(p, order, slots, abort_flag);
+  Walk walk(p, sorted ? order : nullptr, slots, abort_flag);
   Tile x;
   if (warp == 0) {
     // ---------------- TMA producer (both CTAs)
@@ -671,7 +726,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else if (warp == 2 + EPI_WARPS + 1) {
     // ---------------- scheduler (leader)
-    if (leader && lane == 0) schedule_tiles(slots, abort_flag);
+    if (leader && p.dynamic && lane == 0) schedule_tiles(slots, INT32_MAX, abort_flag);
   } else {
     // ---------------- clearing warp: rows behind the group in its last stage
     int kit = 0;
@@ -730,16 +785,18 @@ cudaLaunchConfig_t pair_grid(int64_t pairs, int threads, int smem, cudaStream_t 
 
 template <int NT, bool W_MN, bool F32>
 cudaError_t launch_rows(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& x32,
-                        const RowsParams& p, int T, cudaStream_t st) {
+                        RowsParams p, int T, cudaStream_t st) {
   using C = RowsCfg<NT>;
   auto kern = k_grouped_rows<NT, W_MN, F32>;
   static std::atomic<uint64_t> done{0};
   const LaunchInfo li = launch_info(reinterpret_cast<const void*>(kern), C::SMEM, done);
   if (li.err != cudaSuccess) return li.err;
-  // every group has at most one row tile more than its share of full ones
+  // every group with rows has at most one row tile more than its full ones
   const int64_t tiles = (T / NT + static_cast<int64_t>(p.g.n < T ? p.g.n : T)) * ((p.N + 255) / 256);
+  if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
+  p.dynamic = tiles > li.sms / 2 ? 1 : 0;
   cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = pair_grid(tiles < li.sms / 2 ? tiles : li.sms / 2, C::THREADS, C::SMEM, st, &attr);
+  const cudaLaunchConfig_t cfg = pair_grid(tiles, C::THREADS, C::SMEM, st, &attr);
   return cudaLaunchKernelEx(&cfg, kern, w, x, x32, p);
 }
 
@@ -846,6 +903,7 @@ cudaError_t grouped_wgrad(const void* A, const void* B, const int64_t* offsets, 
   static std::atomic<uint64_t> done{0};
   const LaunchInfo li = launch_info(reinterpret_cast<const void*>(k_grouped_wgrad), GSMEM, done);
   if (li.err != cudaSuccess) return li.err;
+  p.dynamic = tiles > li.sms / 2 ? 1 : 0;
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg = pair_grid(tiles, THREADS, GSMEM, st, &attr);
   return cudaLaunchKernelEx(&cfg, k_grouped_wgrad, a, b, a2, b2, o, p);

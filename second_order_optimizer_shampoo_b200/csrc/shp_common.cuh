@@ -447,18 +447,23 @@ SHP_DEV void tile_slots_init(TileSlots* ts, int consumers) {
   mbar_init(&ts->asked, 1);
 }
 
-// The scheduler, one thread of the leader.  Every wait is bounded.
-SHP_DEV void schedule_tiles(TileSlots* ts, volatile int* abort_flag) {
+// The scheduler, one thread of the leader.  Tiles from `limit` on hold no work
+// (a grid sized by an upper bound): they are cancelled and not passed on.
+// Every wait is bounded.
+SHP_DEV void schedule_tiles(TileSlots* ts, int limit, volatile int* abort_flag) {
   RingPos<2> at;
   uint32_t asked = 0;
   for (;;) {
     if (!ring_wait(smem_u32(&ts->empty[at.slot]), at.parity ^ 1u, abort_flag)) return;
-    mbar_arrive_expect_tx(&ts->asked, 16);
-    try_cancel_cluster(smem_u32(&ts->answer), smem_u32(&ts->asked));
-    if (!ring_wait(smem_u32(&ts->asked), asked, abort_flag)) return;
-    asked ^= 1u;
-    const int cta = cancelled_cta(smem_u32(&ts->answer));
-    fence_proxy_async_smem();  // read before the next answer is written
+    int cta;
+    do {
+      mbar_arrive_expect_tx(&ts->asked, 16);
+      try_cancel_cluster(smem_u32(&ts->answer), smem_u32(&ts->asked));
+      if (!ring_wait(smem_u32(&ts->asked), asked, abort_flag)) return;
+      asked ^= 1u;
+      cta = cancelled_cta(smem_u32(&ts->answer));
+      fence_proxy_async_smem();  // read before the next answer is written
+    } while (cta >= 0 && cta / 2 >= limit);
     for (uint32_t r = 0; r < 2; ++r)
       slot_store(mapa_shared(smem_u32(&ts->tile[at.slot]), r), cta < 0 ? -1 : cta / 2,
                  mapa_shared(smem_u32(&ts->full[at.slot]), r));
