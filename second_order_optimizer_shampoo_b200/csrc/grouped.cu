@@ -48,7 +48,6 @@ SHP_DEV void tma_reduce_add_3d(const CUtensorMap* map, const void* src, int x, i
       : "memory");
 }
 
-SHP_DEV void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 
 // Group e covers the rows [lo, hi): the offsets clamped to 0..T and to
 // non-negative lengths, so that no offset array reaches outside the operands.
@@ -130,11 +129,20 @@ struct RowWalk {
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     return sum;
   }
+  RowTile own;  // the pair's first tile, looked up while the block sets up
+  bool have = false;
+  SHP_DEV void start() { have = find(static_cast<int>(blockIdx.x) / 2, own); }
   SHP_DEV bool next(RowTile& x) {
-    if (!first && !dynamic) return false;
-    const int t = first ? static_cast<int>(blockIdx.x) / 2 : feed.next();
-    first = false;
-    if (t < 0) return false;
+    if (first) {
+      first = false;
+      x = own;
+      return have;
+    }
+    if (!dynamic) return false;
+    const int t = feed.next();
+    return t >= 0 && find(t, x);
+  }
+  SHP_DEV bool find(int t, RowTile& x) {
     if (t < base) e0 = base = 0;
     const int lane = threadIdx.x & 31;
     while (e0 < g.n) {
@@ -247,14 +255,15 @@ __global__ void __launch_bounds__(RowsCfg<NT>::THREADS, 1)
     sort_groups(p.g, order, reinterpret_cast<int*>(smem));
     fence_proxy_async_smem();  // before the copies that reuse the space
   }
+  RowWalk<NT> walk(p.g, p.N, sorted ? order : nullptr, p.dynamic != 0, slots, abort_flag);
+  RowTile x;
+  if (!sorted) walk.start();
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // peer barriers initialised, both TMEM allocations done
   tc_fence_after();
   const uint32_t tmem = uniform(*tmem_slot);
-
-  RowWalk<NT> walk(p.g, p.N, sorted ? order : nullptr, p.dynamic != 0, slots, abort_flag);
-  RowTile x;
+  if (sorted) walk.start();
   if (warp == 0) {
     // ---------------- TMA producer (both CTAs): its 128 columns of W and its
     // half of the tile's rows, in boxes of 32
@@ -429,6 +438,7 @@ __global__ void __launch_bounds__(RowsCfg<NT>::THREADS, 1)
   if (warp == 1) mbar_wait(drain, 0);  // bounded; immediate unless a wait above gave up
   tc_fence_before();
   __syncthreads();
+  // releasing: this CTA's arrivals on the other's barriers land before it exits
   cluster_sync();
   if (warp == 1) tmem_dealloc_pair(tmem, 2 * NT);
 }
@@ -454,7 +464,7 @@ struct WgradParams {
   Groups g;
   int M, N;
   int accumulate;
-  int chunks;   // tA2, tB2 bring both 64-column chunks of a CTA in one box
+  int chunks;   // A and B are mapped as 64-column chunks: both of a CTA in one box
   int dynamic;  // more tiles than pairs: they are handed out
 };
 
@@ -473,18 +483,28 @@ struct Walk {
   const WgradParams& p;
   const uint16_t* order;  // groups by falling size; null: in their own order
   TileFeed feed;
-  int t, tiles_n, per_e;
+  int tiles_n, per_e;
   bool first = true;
   SHP_DEV Walk(const WgradParams& q, const uint16_t* o, TileSlots* ts, volatile int* abort_flag)
-      : p(q), order(o), feed{ts, abort_flag}, t(static_cast<int>(blockIdx.x) / 2) {
+      : p(q), order(o), feed{ts, abort_flag} {
     tiles_n = (q.N + BN - 1) / BN;
     per_e = tiles_n * ((q.M + 255) / 256);
   }
+  Tile own;  // the pair's first tile, looked up while the block sets up
+  SHP_DEV void start() { find(static_cast<int>(blockIdx.x) / 2, own); }
   SHP_DEV bool next(Tile& x) {
-    if (!first && !p.dynamic) return false;
-    if (!first) t = feed.next();
-    first = false;
+    if (first) {
+      first = false;
+      x = own;
+      return true;
+    }
+    if (!p.dynamic) return false;
+    const int t = feed.next();
     if (t < 0) return false;
+    find(t, x);
+    return true;
+  }
+  SHP_DEV void find(int t, Tile& x) const {
     const int i = t / per_e, r = t % per_e;
     x.e = order != nullptr ? uniform(static_cast<int>(order[i])) : i;
     int lo, hi;
@@ -497,14 +517,11 @@ struct Walk {
     x.kb = (hi - lo + BK - 1) / BK;
     x.tail = (hi - lo) % BK;
     x.tail_at = x.tail == 0 ? -1 : max(0, x.kb - 1 - TAIL_EARLY);
-    return true;
   }
 };
 
 __global__ void __launch_bounds__(THREADS, 1)
     k_grouped_wgrad(const __grid_constant__ CUtensorMap tA, const __grid_constant__ CUtensorMap tB,
-                    const __grid_constant__ CUtensorMap tA2,
-                    const __grid_constant__ CUtensorMap tB2,
                     const __grid_constant__ CUtensorMap tO, WgradParams p) {
   count_kernel_run();
   const uint32_t rank = cluster_rank();
@@ -544,8 +561,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     tile_slots_init(slots, 2 * (EPI_WARPS + 2) + 1);
     *abort_flag = 0;
     fence_barrier_init();
-    tma_prefetch_desc(p.chunks ? &tA2 : &tA);
-    tma_prefetch_desc(p.chunks ? &tB2 : &tB);
+    tma_prefetch_desc(&tA);
+    tma_prefetch_desc(&tB);
     tma_prefetch_desc(&tO);
   }
   if (warp == 1) tmem_alloc_pair(tmem_slot, 2 * BN);
@@ -553,14 +570,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     sort_groups(p.g, order, reinterpret_cast<int*>(smem));
     fence_proxy_async_smem();  // before the copies that reuse the space
   }
+  Walk walk(p, sorted ? order : nullptr, slots, abort_flag);
+  Tile x;
+  if (!sorted) walk.start();
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // peer barriers initialised, both TMEM allocations done
   tc_fence_after();
   const uint32_t tmem = uniform(*tmem_slot);
-
-  Walk walk(p, sorted ? order : nullptr, slots, abort_flag);
-  Tile x;
+  if (sorted) walk.start();
   if (warp == 0) {
     // ---------------- TMA producer (both CTAs)
     const uint32_t on = elect_one(), lead = on & (leader ? 1u : 0u);
@@ -583,16 +601,21 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint32_t bar = tail0 + ring.slot * 8;
           const int kt = x.k0 + (x.kb - 1) * BK;
           mbar_expect_tx_if(on, bar, STAGE_BYTES);
-          for (int i = 0; i < 2; ++i) {
-            tma_3d_if(on, sa + i * BK * 128, &tA, bar, m0 + i * 64, kt, 0);
-            tma_3d_if(on, sb + i * BK * 128, &tB, bar, nb0 + i * 64, kt, 0);
+          if (p.chunks) {
+            tma_4d_if(on, sa, &tA, bar, 0, kt, m0 >> 6, 0);
+            tma_4d_if(on, sb, &tB, bar, 0, kt, nb0 >> 6, 0);
+          } else {
+            for (int i = 0; i < 2; ++i) {
+              tma_3d_if(on, sa + i * BK * 128, &tA, bar, m0 + i * 64, kt, 0);
+              tma_3d_if(on, sb + i * BK * 128, &tB, bar, nb0 + i * 64, kt, 0);
+            }
           }
         } else {
           const uint32_t fbar = fleader + ring.slot * 8;
           mbar_expect_tx_if(lead, full0 + ring.slot * 8, 2 * STAGE_BYTES);
           if (p.chunks) {
-            tma_4d_pair_if(on, sa, &tA2, fbar, 0, k0, m0 >> 6, 0);
-            tma_4d_pair_if(on, sb, &tB2, fbar, 0, k0, nb0 >> 6, 0);
+            tma_4d_pair_if(on, sa, &tA, fbar, 0, k0, m0 >> 6, 0);
+            tma_4d_pair_if(on, sb, &tB, fbar, 0, k0, nb0 >> 6, 0);
           } else {
             for (int i = 0; i < 2; ++i) {
               tma_3d_pair_if(on, sa + i * BK * 128, &tA, fbar, m0 + i * 64, k0, 0);
@@ -704,20 +727,25 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int g = 0; g < 4; ++g) {
           const int cb = c0 + g * 32;
           if (cb >= p.N) continue;
-          if (lane == 0) bulk_wait_read_all();  // the last store has read the box
-          __syncwarp();
+          // the warp's box, or, when no more tiles come, a box of its own for
+          // each store in the stages, which nothing reads or fills any more
+          uint8_t* bx = p.dynamic ? box : smem + ((warp - 2) * 4 + g) * EPI_BOX;
+          if (p.dynamic) {
+            if (lane == 0) bulk_wait_read_all();  // the last store has read the box
+            __syncwarp();
+          }
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<float4*>(box + sw128_off(lane, i)) =
+            *reinterpret_cast<float4*>(bx + sw128_off(lane, i)) =
                 make_float4(acc[g * 32 + 4 * i], acc[g * 32 + 4 * i + 1], acc[g * 32 + 4 * i + 2],
                             acc[g * 32 + 4 * i + 3]);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
             if (p.accumulate)
-              tma_reduce_add_3d(&tO, box, cb, row0, x.e);
+              tma_reduce_add_3d(&tO, bx, cb, row0, x.e);
             else
-              tma_store_3d(&tO, box, cb, row0, x.e);
+              tma_store_3d(&tO, bx, cb, row0, x.e);
             bulk_commit();
           }
         }
@@ -751,8 +779,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!leader) {
         if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&clearb[s]), 0));
       } else {
-        if (!warp_wait(smem_u32(&clearb[s]), (par >> s) & 1, abort_flag)) break;
-        fence_cluster();
+        if (!warp_wait_cluster(smem_u32(&clearb[s]), (par >> s) & 1, abort_flag)) break;
         if (lane == 0) mbar_arrive(&full[s]);
       }
       par ^= 1u << s;
@@ -762,6 +789,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp == 1) mbar_wait(drain, 0);  // bounded; immediate unless a wait above gave up
   tc_fence_before();
   __syncthreads();
+  // releasing: this CTA's arrivals on the other's barriers land before it exits
   cluster_sync();
   if (warp == 1) tmem_dealloc_pair(tmem, 2 * BN);
 }
@@ -873,27 +901,25 @@ cudaError_t grouped_rows(const void* X, const int64_t* offsets, const void* W, b
 
 cudaError_t grouped_wgrad(const void* A, const void* B, const int64_t* offsets, float* G, int T,
                           int M, int N, int groups, bool accumulate, cudaStream_t st) {
-  CUtensorMap a, b, o;
-  bool ok = true;
-  if (T > 0) {
-    ok = tensor_map(&a, A, 2, M, T, 1, M, 0, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B) &&
-         tensor_map(&b, B, 2, N, T, 1, N, 0, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B);
-  }
-  ok = ok && tensor_map(&o, G, 4, N, M, groups, N, static_cast<int64_t>(M) * N, 32, 32,
-                        CU_TENSOR_MAP_SWIZZLE_128B);
-  if (!ok) return cudaErrorInvalidValue;
-  if (T == 0) a = b = o;  // no group has a row: never loaded from
   WgradParams p;
   memset(&p, 0, sizeof(p));
-  CUtensorMap a2 = a, b2 = b;
-  if (T > 0 && M % 64 == 0 && N % 64 == 0) {
+  CUtensorMap a, b, o;
+  bool ok = tensor_map(&o, G, 4, N, M, groups, N, static_cast<int64_t>(M) * N, 32, 32,
+                       CU_TENSOR_MAP_SWIZZLE_128B);
+  if (T == 0) {
+    a = b = o;  // no group has a row: never loaded from
+  } else if (M % 64 == 0 && N % 64 == 0) {
     p.chunks = 1;
-    if (!tensor_map4(&a2, A, 2, {64, T, M / 64, 1}, {M, 64, static_cast<int64_t>(T) * M},
-                     {64, BK, 2, 1}, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !tensor_map4(&b2, B, 2, {64, T, N / 64, 1}, {N, 64, static_cast<int64_t>(T) * N},
-                     {64, BK, 2, 1}, CU_TENSOR_MAP_SWIZZLE_128B))
-      return cudaErrorInvalidValue;
+    ok = ok &&
+         tensor_map4(&a, A, 2, {64, T, M / 64, 1}, {M, 64, static_cast<int64_t>(T) * M},
+                     {64, BK, 2, 1}, CU_TENSOR_MAP_SWIZZLE_128B) &&
+         tensor_map4(&b, B, 2, {64, T, N / 64, 1}, {N, 64, static_cast<int64_t>(T) * N},
+                     {64, BK, 2, 1}, CU_TENSOR_MAP_SWIZZLE_128B);
+  } else {
+    ok = ok && tensor_map(&a, A, 2, M, T, 1, M, 0, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B) &&
+         tensor_map(&b, B, 2, N, T, 1, N, 0, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B);
   }
+  if (!ok) return cudaErrorInvalidValue;
   p.g = Groups{offsets, groups, T};
   p.M = M;
   p.N = N;
@@ -906,7 +932,7 @@ cudaError_t grouped_wgrad(const void* A, const void* B, const int64_t* offsets, 
   p.dynamic = tiles > li.sms / 2 ? 1 : 0;
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg = pair_grid(tiles, THREADS, GSMEM, st, &attr);
-  return cudaLaunchKernelEx(&cfg, k_grouped_wgrad, a, b, a2, b2, o, p);
+  return cudaLaunchKernelEx(&cfg, k_grouped_wgrad, a, b, o, p);
 }
 
 uint64_t kernel_runs_grouped() {

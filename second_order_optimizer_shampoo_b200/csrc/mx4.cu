@@ -634,6 +634,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp == 1) mbar_wait(drain, 0);  // bounded; immediate unless a wait above gave up
   tc_fence_before();
   __syncthreads();
+  // releasing: this CTA's arrivals on the other's barriers land before it exits
   cluster_sync();
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }

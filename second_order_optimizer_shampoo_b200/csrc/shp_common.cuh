@@ -116,6 +116,23 @@ SHP_DEV bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) 
   return __all_sync(0xffffffffu, ring_wait(bar, parity, abort_flag));
 }
 
+// warp_wait that also acquires what the other CTA of the pair released.
+SHP_DEV bool warp_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  bool ok = ring_wait(bar, parity, abort_flag);
+  if (ok) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    ok = done != 0;
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
 // Limit of the wait a bounded-wait self-test points at a barrier nothing
 // completes (about 10 ms): long enough to be a real wait, short for a test.
 #define SHP_SELFTEST_LIMIT (20000000LL)
@@ -355,6 +372,15 @@ SHP_DEV void tma_3d_if(uint32_t on, uint32_t dst, const CUtensorMap* map, uint32
       "@q cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
       " [%1], [%2, {%4, %5, %6}], [%3];\n\t}" ::"r"(on),
       "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(mbar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+SHP_DEV void tma_4d_if(uint32_t on, uint32_t dst, const CUtensorMap* map, uint32_t mbar, int x,
+                       int y, int z, int w) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
+      "@q cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%1], [%2, {%4, %5, %6, %7}], [%3];\n\t}" ::"r"(on),
+      "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(mbar), "r"(x), "r"(y), "r"(z), "r"(w)
       : "memory");
 }
 SHP_DEV void tma_3d_pair_if(uint32_t on, uint32_t dst, const CUtensorMap* map, uint32_t mbar,
