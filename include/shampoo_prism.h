@@ -321,10 +321,14 @@ int shp_split_tf32(const float* X, int64_t count, float* hi, float* lo, shp_stre
  * rows offsets[e] .. offsets[e+1]-1 of a [T][...] matrix.  `offsets` is a
  * DEVICE array of groups + 1 int64, non-decreasing and within 0..T; it is read
  * by the kernels, nothing waits for the host, and any group may be empty.
- * Offsets outside 0..T are clamped and a decreasing pair counts as an empty
- * group, so no value of them reaches outside the operands.  Operands are bf16,
- * sums fp32; K, N, m, n are multiples of 8; T and the groups' sizes are
- * arbitrary.  groups <= 65535.  No workspace. */
+ * Other offsets give unspecified results, but reach nothing outside the
+ * operands: they are clamped to 0..T, and a decreasing pair counts as an empty
+ * group.  Operands are bf16, sums fp32; K, N, m, n are multiples of 8; T and
+ * the groups' sizes are arbitrary.  groups <= 65535.  No workspace.
+ *
+ * These products and those of the 4-bit format below have no status to report:
+ * a bounded wait inside their kernels that ran out (only a device fault can
+ * cause that) leaves the result incomplete, as in shp_matmul. */
 
 /* Y[t] = X[t] W[e(t)] for every row t of every group: the forward product of
  * an expert layer, and with the other w_trans the gradient of its input.

@@ -495,6 +495,8 @@ int shp_grouped_matmul(const void* X, const int64_t* offsets, const void* W, int
   if (K % 8 || N % 8) return SHP_EINVAL;
   if (!aligned16(X) || !aligned16(W) || !aligned16(Y) || !aligned8(offsets)) return SHP_EINVAL;
   if (T > kMaxRows || K > kMaxRows || N > kMaxRows || groups > 65535) return SHP_EUNSUPPORTED;
+  // tiles are numbered in 32 bits (at least 64 rows by 256 columns each)
+  if ((T / 64 + groups) > INT32_MAX / 2 / ((N + 255) / 256)) return SHP_EUNSUPPORTED;
   if (T == 0) return SHP_OK;
   CK(grouped_rows(X, offsets, W, w_trans != 0, Y, static_cast<int>(T), static_cast<int>(K),
                   static_cast<int>(N), static_cast<int>(groups), out_storage == SHP_TF32,
@@ -509,6 +511,7 @@ int shp_grouped_wgrad(const void* A, const void* B, const int64_t* offsets, floa
   if (m % 8 || n % 8) return SHP_EINVAL;
   if (!aligned16(A) || !aligned16(B) || !aligned16(G) || !aligned8(offsets)) return SHP_EINVAL;
   if (T > kMaxRows || m > kMaxRows || n > kMaxRows || groups > 65535) return SHP_EUNSUPPORTED;
+  if (groups * ((m + 255) / 256) > INT32_MAX / 2 / ((n + 255) / 256)) return SHP_EUNSUPPORTED;
   CK(grouped_wgrad(A, B, offsets, G, static_cast<int>(T), static_cast<int>(m),
                    static_cast<int>(n), static_cast<int>(groups), accumulate != 0,
                    static_cast<cudaStream_t>(stream)));

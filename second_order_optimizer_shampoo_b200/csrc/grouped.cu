@@ -89,8 +89,8 @@ struct RowTile {
   int e, t0, count, n0;
 };
 
-// A role's walk over its pair's tiles: its own, then, in a grid of more tiles
-// than pairs, the ones the scheduler passes on.  Tiles are numbered over the
+// A role's walk over its pair's tiles: its own, then the ones the scheduler
+// passes on, or, where not dynamic, every gridDim / 2-th.  Tiles are numbered over the
 // groups in order (by falling size where sorted); a group of len rows has
 // ceil(len / NT) row tiles of equal size (up to the MMA's granule of 16), each
 // with every column tile.  next() is called by whole warps and looks at 32
@@ -131,15 +131,16 @@ struct RowWalk {
   }
   RowTile own;  // the pair's first tile, looked up while the block sets up
   bool have = false;
-  SHP_DEV void start() { have = find(static_cast<int>(blockIdx.x) / 2, own); }
+  int turn = static_cast<int>(blockIdx.x) / 2;
+  SHP_DEV void start() { have = find(turn, own); }
   SHP_DEV bool next(RowTile& x) {
     if (first) {
       first = false;
       x = own;
       return have;
     }
-    if (!dynamic) return false;
-    const int t = feed.next();
+    turn += static_cast<int>(gridDim.x) / 2;
+    const int t = dynamic ? feed.next() : turn;
     return t >= 0 && find(t, x);
   }
   SHP_DEV bool find(int t, RowTile& x) {
@@ -181,9 +182,8 @@ struct RowWalk {
 // of the group its N, any multiple of 16 up to NT.  So the time of the MMAs
 // follows the rows a group has, and few rows cost little more than streaming
 // W; with the rows as M = 256 a single row cost as much as 256.
-// NT (64, 128 or 256 rows) sets the ring: a stage is 16 KB of W and up to
-// NT * 64 bytes of X per CTA, so small tiles leave room for more stages of W in
-// flight.  The launcher picks it from the mean number of rows per group.
+// NT (64, 128 or 256 rows; rows_per_tile()) is a tile's height: a stage is 16 KB
+// of W and up to NT * 64 bytes of X per CTA.
 // Epilogue: a lane holds one column of Y; for fp32 results 32 lanes store 128
 // contiguous bytes of a row, for bf16 lanes trade halves so that 16 lanes store
 // 64, directly and only inside the group.
@@ -191,7 +191,7 @@ struct RowsParams {
   Groups g;
   int N, K;
   int w_chunks;  // W [K][N] is mapped as 64-column chunks: both of a CTA in one box
-  int dynamic;   // more tiles than pairs: they are handed out, the largest groups' first
+  int dynamic;   // tiles are handed out, the largest groups' first; else taken in turn
   void* out;
 };
 
@@ -821,10 +821,15 @@ cudaError_t launch_rows(const CUtensorMap& w, const CUtensorMap& x, const CUtens
   if (li.err != cudaSuccess) return li.err;
   // every group with rows has at most one row tile more than its full ones
   const int64_t tiles = (T / NT + static_cast<int64_t>(p.g.n < T ? p.g.n : T)) * ((p.N + 255) / 256);
-  if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
-  p.dynamic = tiles > li.sms / 2 ? 1 : 0;
+  // Handing tiles out pays where their rows, and so their times, differ: 16
+  // skewed groups of about 192 rows, 4096 x 1024, 52 us against 76 in turn.  Few
+  // rows per group cost the same everywhere, and putting the groups in order is
+  // in the way: 16 rows over 64 groups, 1024 x 4096, 26.4 us against 25.6.
+  const int64_t pairs = li.sms / 2;
+  p.dynamic = tiles > pairs && T > 32 * static_cast<int64_t>(p.g.n) ? 1 : 0;
   cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = pair_grid(tiles, C::THREADS, C::SMEM, st, &attr);
+  const cudaLaunchConfig_t cfg =
+      pair_grid(p.dynamic || tiles < pairs ? tiles : pairs, C::THREADS, C::SMEM, st, &attr);
   return cudaLaunchKernelEx(&cfg, kern, w, x, x32, p);
 }
 
@@ -925,7 +930,6 @@ cudaError_t grouped_wgrad(const void* A, const void* B, const int64_t* offsets, 
   p.N = N;
   p.accumulate = accumulate ? 1 : 0;
   const int64_t tiles = static_cast<int64_t>(groups) * ((M + 255) / 256) * ((N + BN - 1) / BN);
-  if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
   static std::atomic<uint64_t> done{0};
   const LaunchInfo li = launch_info(reinterpret_cast<const void*>(k_grouped_wgrad), GSMEM, done);
   if (li.err != cudaSuccess) return li.err;

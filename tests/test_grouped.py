@@ -42,6 +42,9 @@ def test_sizes_beyond_the_tile_coordinates():
         assert rows(**kw) == A.SHP_EUNSUPPORTED
     for kw in (dict(T=big), dict(m=big), dict(n=big), dict(E=65536)):
         assert wgrad(**kw) == A.SHP_EUNSUPPORTED
+    # more tiles than 32 bits number
+    assert rows(T=2 ** 30, N=2 ** 30) == A.SHP_EUNSUPPORTED
+    assert wgrad(m=2 ** 24, n=2 ** 24, E=65535) == A.SHP_EUNSUPPORTED
 
 
 def test_no_rows_launches_nothing():
