@@ -324,6 +324,7 @@ def _want(name, t, dtype, shape):
         raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
 
 
+_BF16 = torch.bfloat16
 _STORAGE = {torch.bfloat16: A.SHP_BF16, torch.float32: A.SHP_TF32}
 
 
@@ -354,9 +355,12 @@ def shp_grouped_matmul(X, offsets, W, w_trans=False, out=None, dtype=torch.bfloa
     if X.dim() != 2 or W.dim() != 3:
         raise ValueError("X is [T, K] and W [groups, K, N]")
     T, K = X.shape
-    groups, N = W.shape[0], W.shape[1 if w_trans else 2]
-    _want("X", X, torch.bfloat16, (T, K))
-    _want("W", W, torch.bfloat16, (groups, N, K) if w_trans else (groups, K, N))
+    groups, N, k = W.shape
+    if not w_trans:
+        N, k = k, N
+    if k != K or X.dtype != _BF16 or W.dtype != _BF16:
+        _want("X", X, _BF16, (T, K))
+        _want("W", W, _BF16, (groups, N, K) if w_trans else (groups, K, N))
     _want("offsets", offsets, torch.int64, (groups + 1,))
     out, storage = _result(out, (T, N), dtype, X.device)
     _check(A.lib().shp_grouped_matmul(X.data_ptr(), offsets.data_ptr(), W.data_ptr(),
@@ -379,8 +383,8 @@ def shp_grouped_wgrad(Amat, B, offsets, out=None, accumulate=False):
         raise ValueError("accumulate needs out")
     T, m = Amat.shape
     n, groups = B.shape[1], offsets.shape[0] - 1
-    _want("A", Amat, torch.bfloat16, (T, m))
-    _want("B", B, torch.bfloat16, (T, n))
+    _want("A", Amat, _BF16, (T, m))
+    _want("B", B, _BF16, (T, n))
     _want("offsets", offsets, torch.int64, (groups + 1,))
     if out is None:
         out = torch.empty((groups, m, n), dtype=torch.float32, device=B.device)

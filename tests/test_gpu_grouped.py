@@ -202,6 +202,61 @@ def test_repeats_are_identical_and_streams_independent():
         assert torch.equal(y, Y1) and torch.equal(gr, G1)
 
 
+@pytest.mark.parametrize("T,E,K,N", [(20000, 200, 136, 520), (15000, 300, 72, 328), (70000, 16, 64, 1032)])
+def test_more_tiles_than_sm_pairs(T, E, K, N):
+    """Tiles handed out at run time, the groups sorted by size (up to 256 of
+    them) or not, some empty, sizes far apart; and every repeat the same."""
+    g = gen(12)
+    p = torch.rand(E, generator=torch.Generator().manual_seed(4)).pow(6)
+    sizes = torch.bincount(torch.multinomial(p, T, replacement=True, generator=torch.Generator().manual_seed(5)),
+                           minlength=E).tolist()
+    edges = [0]
+    for n in sizes:
+        edges.append(edges[-1] + n)
+    assert 0 in sizes and max(sizes) > 256
+    X, W, B = rnd(g, T, K), rnd(g, E, K, N, scale=0.1), rnd(g, T, N)
+    off = offs(edges)
+    for dtype in (torch.bfloat16, torch.float32):
+        Y = P().shp_grouped_matmul(X, off, W, dtype=dtype)
+        check_rows(X, edges, W, False, Y, Y)
+        for _ in range(3):
+            assert torch.equal(P().shp_grouped_matmul(X, off, W, dtype=dtype), Y)
+    G = P().shp_grouped_wgrad(X, B, off)
+    check_wgrad(X, B, edges, G)
+    for _ in range(3):
+        assert torch.equal(P().shp_grouped_wgrad(X, B, off), G)
+
+
+def test_two_captured_graphs_at_once():
+    """Two graphs of the same calls on other tensors, replayed together on two
+    streams: nothing is shared between them."""
+    g = gen(13)
+    T, K, N, E = 6000, 264, 520, 40
+    edges = [0] + sorted(torch.randint(0, T, (E - 1,), generator=torch.Generator().manual_seed(6)).tolist()) + [T]
+    off = offs(edges)
+    sides = []
+    for _ in range(2):
+        X, W, B = rnd(g, T, K), rnd(g, E, K, N, scale=0.1), rnd(g, T, N)
+        Y = torch.zeros(T, N, dtype=torch.bfloat16, device="cuda")
+        G = torch.zeros(E, K, N, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        P().shp_grouped_matmul(X, off, W, out=Y)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            P().shp_grouped_matmul(X, off, W, out=Y)
+            P().shp_grouped_wgrad(X, B, off, out=G)
+        sides.append((graph, X, W, B, Y, G))
+    streams = [torch.cuda.Stream() for _ in sides]
+    for _ in range(5):
+        for s, side in zip(streams, sides):
+            with torch.cuda.stream(s):
+                side[0].replay()
+    torch.cuda.synchronize()
+    for _, X, W, B, Y, G in sides:
+        check_rows(X, edges, W, False, Y, Y)
+        check_wgrad(X, B, edges, G)
+
+
 def test_captured_calls_follow_the_offsets():
     """A captured graph reads the offsets on the device: a replay with other
     boundaries and rows gives their results."""
