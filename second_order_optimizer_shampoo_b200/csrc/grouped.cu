@@ -39,6 +39,7 @@ constexpr int BK = 64;                // contraction elements per stage: 128-byt
 constexpr int A_BYTES = 128 * 128;    // per CTA and stage: 128 rows (columns) of A
 constexpr int CHUNK_KB = 8;  // stages per fp32 chunk: sums of 512 products inside the tensor core
 constexpr int EPI_WARPS = 8;
+constexpr int EPI_BOX = 4096;  // one warp's 32 x 32 fp32 store box
 
 SHP_DEV void tma_reduce_add_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
   asm volatile(
@@ -184,9 +185,12 @@ struct RowWalk {
 // W; with the rows as M = 256 a single row cost as much as 256.
 // NT (64, 128 or 256 rows; rows_per_tile()) is a tile's height: a stage is 16 KB
 // of W and up to NT * 64 bytes of X per CTA.
-// Epilogue: a lane holds one column of Y; for fp32 results 32 lanes store 128
-// contiguous bytes of a row, for bf16 lanes trade halves so that 16 lanes store
-// 64, directly and only inside the group.
+// Epilogue: a lane holds one column of Y.  bf16: lanes trade halves so that 16
+// lanes store 64 contiguous bytes of a row, directly and only inside the group.
+// fp32: whole 32-row chunks go through shared memory and leave as bulk stores
+// (stored directly, 4 bytes per lane, a 256 x 256 tile took 9700 clocks of
+// stores, more than the MMAs of K = 1024: 65536 rows x 1024 x 4096 590 us, now 481),
+// partial ones directly.
 struct RowsParams {
   Groups g;
   int N, K;
@@ -195,22 +199,24 @@ struct RowsParams {
   void* out;
 };
 
-template <int NT>
+template <int NT, bool F32>
 struct RowsCfg {
   static constexpr int X_BYTES = NT / 2 * 128;
   static constexpr int STAGE = A_BYTES + X_BYTES;
-  static constexpr int TAIL = 320 + static_cast<int>(sizeof(TileSlots)) + SORT_MAX * 2;
+  static constexpr int BOXES = F32 ? EPI_WARPS * EPI_BOX : 0;
+  static constexpr int TAIL = BOXES + 320 + static_cast<int>(sizeof(TileSlots)) + SORT_MAX * 2;
   static constexpr int STAGES = (232448 - 1024 - TAIL) / STAGE;
   static constexpr int SMEM = 1024 + STAGES * STAGE + TAIL;
   static constexpr int THREADS = 32 * (2 + EPI_WARPS + 1);
 };
 
 template <int NT, bool W_MN, bool F32>
-__global__ void __launch_bounds__(RowsCfg<NT>::THREADS, 1)
+__global__ void __launch_bounds__(RowsCfg<NT, F32>::THREADS, 1)
     k_grouped_rows(const __grid_constant__ CUtensorMap tW, const __grid_constant__ CUtensorMap tX,
-                   const __grid_constant__ CUtensorMap tX32, RowsParams p) {
+                   const __grid_constant__ CUtensorMap tX32,
+                   const __grid_constant__ CUtensorMap tY, RowsParams p) {
   count_kernel_run();
-  using C = RowsCfg<NT>;
+  using C = RowsCfg<NT, F32>;
   constexpr int STAGES = C::STAGES;
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
@@ -219,7 +225,8 @@ __global__ void __launch_bounds__(RowsCfg<NT>::THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  TileSlots* slots = reinterpret_cast<TileSlots*>(smem + STAGES * C::STAGE);
+  uint8_t* boxes = smem + STAGES * C::STAGE;
+  TileSlots* slots = reinterpret_cast<TileSlots*>(boxes + C::BOXES);
   uint64_t* full = reinterpret_cast<uint64_t*>(slots + 1);
   uint64_t* empty = full + STAGES;
   uint64_t* accf = empty + STAGES;
@@ -249,6 +256,7 @@ __global__ void __launch_bounds__(RowsCfg<NT>::THREADS, 1)
     tma_prefetch_desc(&tW);
     tma_prefetch_desc(&tX);
     tma_prefetch_desc(&tX32);
+    if (F32) tma_prefetch_desc(&tY);
   }
   if (warp == 1) tmem_alloc_pair(tmem_slot, 2 * NT);
   if (sorted) {
@@ -395,14 +403,30 @@ __global__ void __launch_bounds__(RowsCfg<NT>::THREADS, 1)
           if (lane == 0) mbar_arrive_relaxed(mapa_shared(smem_u32(&acce[u]), 0));
         }
         if (stop) break;
-        if (nb + lane < p.N) {
+        if (nb < p.N) {
+          uint8_t* box = boxes + (warp - 2) * EPI_BOX;
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
             const int r0 = (2 * c + h) * 32;
-            float* o = static_cast<float*>(p.out) + static_cast<int64_t>(x.t0 + r0) * p.N + nb + lane;
+            if (r0 + 32 <= x.count) {  // whole chunks leave as bulk stores
+              if (lane == 0) bulk_wait_read_all();  // the last store has read the box
+              __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (r0 + j < x.count) o[static_cast<int64_t>(j) * p.N] = acc[c * 32 + j];
+              for (int j = 0; j < 32; ++j)
+                *reinterpret_cast<float*>(box + sw128_off(j, lane >> 2) + (lane & 3) * 4) =
+                    acc[c * 32 + j];
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_3d(&tY, box, nb, x.t0 + r0, 0);
+                bulk_commit();
+              }
+            } else if (r0 < x.count && nb + lane < p.N) {
+              float* o = static_cast<float*>(p.out) + static_cast<int64_t>(x.t0 + r0) * p.N + nb + lane;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (r0 + j < x.count) o[static_cast<int64_t>(j) * p.N] = acc[c * 32 + j];
+            }
           }
         }
       } else {
@@ -433,6 +457,10 @@ __global__ void __launch_bounds__(RowsCfg<NT>::THREADS, 1)
         if (lane == 0) mbar_arrive_relaxed(mapa_shared(smem_u32(&acce[u]), 0));
       }
     }
+    if (F32) {
+      if (lane == 0) bulk_wait_all();  // nothing outlives the CTA's shared memory
+      __syncwarp();
+    }
   }
 
   if (warp == 1) mbar_wait(drain, 0);  // bounded; immediate unless a wait above gave up
@@ -455,7 +483,6 @@ constexpr int STAGE_BYTES = 2 * A_BYTES;
 constexpr int STAGES = 6;
 constexpr int BN = 256;
 constexpr int THREADS = 32 * (2 + EPI_WARPS + 2);
-constexpr int EPI_BOX = 4096;  // one warp's 32 x 32 store box
 constexpr int GSMEM = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * EPI_BOX + 320 +
                       static_cast<int>(sizeof(TileSlots)) + SORT_MAX * 2;
 static_assert(GSMEM <= 232448, "weight-gradient kernel exceeds shared memory");
@@ -813,8 +840,8 @@ cudaLaunchConfig_t pair_grid(int64_t pairs, int threads, int smem, cudaStream_t 
 
 template <int NT, bool W_MN, bool F32>
 cudaError_t launch_rows(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& x32,
-                        RowsParams p, int T, cudaStream_t st) {
-  using C = RowsCfg<NT>;
+                        const CUtensorMap& y, RowsParams p, int T, cudaStream_t st) {
+  using C = RowsCfg<NT, F32>;
   auto kern = k_grouped_rows<NT, W_MN, F32>;
   static std::atomic<uint64_t> done{0};
   const LaunchInfo li = launch_info(reinterpret_cast<const void*>(kern), C::SMEM, done);
@@ -830,21 +857,24 @@ cudaError_t launch_rows(const CUtensorMap& w, const CUtensorMap& x, const CUtens
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg =
       pair_grid(p.dynamic || tiles < pairs ? tiles : pairs, C::THREADS, C::SMEM, st, &attr);
-  return cudaLaunchKernelEx(&cfg, kern, w, x, x32, p);
+  return cudaLaunchKernelEx(&cfg, kern, w, x, x32, y, p);
 }
 
 template <int NT>
 cudaError_t dispatch_rows(const void* X, const CUtensorMap& w, bool w_mn, bool f32,
                           const RowsParams& p, int T, cudaStream_t st) {
-  CUtensorMap x, x32;
+  CUtensorMap x, x32, y;
+  memset(&y, 0, sizeof(y));
+  if (f32 && !tensor_map(&y, p.out, 4, p.N, T, 1, p.N, 0, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
   if (!tensor_map(&x, X, 2, p.K, T, 1, p.K, 0, BK, NT / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !tensor_map(&x32, X, 2, p.K, T, 1, p.K, 0, BK, 32, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   if (w_mn)
-    return f32 ? launch_rows<NT, true, true>(w, x, x32, p, T, st)
-               : launch_rows<NT, true, false>(w, x, x32, p, T, st);
-  return f32 ? launch_rows<NT, false, true>(w, x, x32, p, T, st)
-             : launch_rows<NT, false, false>(w, x, x32, p, T, st);
+    return f32 ? launch_rows<NT, true, true>(w, x, x32, y, p, T, st)
+               : launch_rows<NT, true, false>(w, x, x32, y, p, T, st);
+  return f32 ? launch_rows<NT, false, true>(w, x, x32, y, p, T, st)
+             : launch_rows<NT, false, false>(w, x, x32, y, p, T, st);
 }
 
 // Rows per tile.  The host knows the mean size of a group only, so it counts as
