@@ -90,66 +90,29 @@ struct RowTile {
   int e, t0, count, n0;
 };
 
-// A role's walk over its pair's tiles: its own, then the ones the scheduler
-// passes on, or, where not dynamic, every gridDim / 2-th.  Tiles are numbered over the
-// groups in order (by falling size where sorted); a group of len rows has
-// ceil(len / NT) row tiles of equal size (up to the MMA's granule of 16), each
-// with every column tile.  next() is called by whole warps and looks at 32
-// groups per step.
+// Looks row tiles up by number.  Tiles are numbered over the groups in order (by
+// falling size where sorted); a group of len rows has ceil(len / NT) row tiles
+// of equal size (up to the MMA's granule of 16), each with every column tile.
+// find() is called by whole warps and looks at 32 groups per step.
 template <int NT>
-struct RowWalk {
+struct RowTiles {
   const Groups g;
   const uint16_t* order;  // null: the groups in their own order
-  const bool dynamic;
   const int tiles_n;
-  TileFeed feed;
-  bool first = true;
   int e0 = 0;    // first group of the window
   int base = 0;  // tiles before the window
-  SHP_DEV RowWalk(const Groups& groups, int N, const uint16_t* o, bool dyn, TileSlots* ts,
-                  volatile int* abort_flag)
-      : g(groups), order(o), dynamic(dyn), tiles_n((N + 255) / 256), feed{ts, abort_flag} {}
-  // Group number, rows and tiles of the lane's group of the window.
-  SHP_DEV int window(int lane, int& a, int& b, int& e) const {
-    a = b = 0;
-    e = e0 + lane;
-    if (e < g.n) {
-      if (order != nullptr) e = order[e];
-      g.range(e, a, b);
-    }
-    return (b - a + NT - 1) / NT * tiles_n;
-  }
-  SHP_DEV int total() {  // all tiles (whole warp; leaves the walk at its start)
-    int sum = 0;
-    for (e0 = 0; e0 < g.n; e0 += 32) {
-      int a, b, e;
-      sum += window(threadIdx.x & 31, a, b, e);
-    }
-    e0 = 0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    return sum;
-  }
-  RowTile own;  // the pair's first tile, looked up while the block sets up
-  bool have = false;
-  int turn = static_cast<int>(blockIdx.x) / 2;
-  SHP_DEV void start() { have = find(turn, own); }
-  SHP_DEV bool next(RowTile& x) {
-    if (first) {
-      first = false;
-      x = own;
-      return have;
-    }
-    turn += static_cast<int>(gridDim.x) / 2;
-    const int t = dynamic ? feed.next() : turn;
-    return t >= 0 && find(t, x);
-  }
+  SHP_DEV RowTiles(const Groups& groups, int N, const uint16_t* o)
+      : g(groups), order(o), tiles_n((N + 255) / 256) {}
   SHP_DEV bool find(int t, RowTile& x) {
     if (t < base) e0 = base = 0;
     const int lane = threadIdx.x & 31;
     while (e0 < g.n) {
-      int a, b, e;
-      const int cnt = window(lane, a, b, e);
+      int a = 0, b = 0, e = e0 + lane;
+      if (e < g.n) {
+        if (order != nullptr) e = order[e];
+        g.range(e, a, b);
+      }
+      const int cnt = (b - a + NT - 1) / NT * tiles_n;
       int inc = cnt;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -173,6 +136,29 @@ struct RowWalk {
       e0 += 32;
     }
     return false;  // a number beyond the last tile
+  }
+};
+
+// A role's walk over its pair's tiles: its own, which every role looks up while
+// the block sets up, then the scheduler's.
+struct RowWalk {
+  TileFeed feed;
+  RowTile own;
+  bool have, first = true;
+  SHP_DEV RowWalk(TileSlots* ts, volatile int* abort_flag) : feed{ts, abort_flag}, have(false) {}
+  SHP_DEV bool next(RowTile& x) {
+    if (first) {
+      first = false;
+      x = own;
+      return have;
+    }
+    int v[8];
+    feed.next(v);
+    x.e = v[0];
+    x.t0 = v[1];
+    x.count = v[2];
+    x.n0 = v[3];
+    return x.e >= 0;
   }
 };
 
@@ -263,15 +249,17 @@ __global__ void __launch_bounds__(RowsCfg<NT, F32>::THREADS, 1)
     sort_groups(p.g, order, reinterpret_cast<int*>(smem));
     fence_proxy_async_smem();  // before the copies that reuse the space
   }
-  RowWalk<NT> walk(p.g, p.N, sorted ? order : nullptr, p.dynamic != 0, slots, abort_flag);
+  RowTiles<NT> tiles(p.g, p.N, sorted ? order : nullptr);
+  RowWalk walk(slots, abort_flag);
   RowTile x;
-  if (!sorted) walk.start();
+  const int turn = static_cast<int>(blockIdx.x) / 2;
+  if (!sorted) walk.have = tiles.find(turn, walk.own);
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // peer barriers initialised, both TMEM allocations done
   tc_fence_after();
   const uint32_t tmem = uniform(*tmem_slot);
-  if (sorted) walk.start();
+  if (sorted) walk.have = tiles.find(turn, walk.own);
   if (warp == 0) {
     // ---------------- TMA producer (both CTAs): its 128 columns of W and its
     // half of the tile's rows, in boxes of 32
@@ -362,11 +350,18 @@ __global__ void __launch_bounds__(RowsCfg<NT, F32>::THREADS, 1)
     }
   } else if (warp == 2 + EPI_WARPS) {
     // ---------------- scheduler (leader)
-    if (leader && p.dynamic) {
-      const int total = uniform(walk.total());
-      if (lane == 0 && static_cast<int>(blockIdx.x) / 2 < total)
-        schedule_tiles(slots, total, abort_flag);
-    }
+    if (leader && walk.have)
+      schedule_tiles(
+          slots, p.dynamic != 0, turn, static_cast<int>(gridDim.x) / 2,
+          [&](int t, int(&v)[8]) {
+            if (!tiles.find(t, x)) return false;
+            v[0] = x.e;
+            v[1] = x.t0;
+            v[2] = x.count;
+            v[3] = x.n0;
+            return true;
+          },
+          abort_flag);
   } else {
     // ---------------- epilogue warps (both CTAs, each on its TMEM rows): warp
     // (q, h) takes the W columns of lane quarter q and the 32-row chunks
@@ -502,48 +497,54 @@ struct WgradParams {
 // last: 64 groups of 250 rows, 1024 x 1024: 77 -> 72 us (of 256 rows: 64 us).
 constexpr int TAIL_EARLY = STAGES - 2;  // the stages behind it still fit in the ring
 struct Tile {
-  int e, m0, n0, k0, kb, tail, tail_at;
+  int e, m0, n0, k0, len, kb, tail, tail_at;
 };
 
-// A role's walk over its pair's tiles.
+// A role's walk over its pair's tiles: its own, then the scheduler's.
 struct Walk {
   const WgradParams& p;
   const uint16_t* order;  // groups by falling size; null: in their own order
   TileFeed feed;
   int tiles_n, per_e;
   bool first = true;
+  Tile own;
   SHP_DEV Walk(const WgradParams& q, const uint16_t* o, TileSlots* ts, volatile int* abort_flag)
       : p(q), order(o), feed{ts, abort_flag} {
     tiles_n = (q.N + BN - 1) / BN;
     per_e = tiles_n * ((q.M + 255) / 256);
   }
-  Tile own;  // the pair's first tile, looked up while the block sets up
-  SHP_DEV void start() { find(static_cast<int>(blockIdx.x) / 2, own); }
+  SHP_DEV bool find(int t, Tile& x) const {
+    if (t >= per_e * p.g.n) return false;
+    const int i = t / per_e, r = t % per_e;
+    x.e = order != nullptr ? uniform(static_cast<int>(order[i])) : i;
+    int lo, hi;
+    p.g.range(x.e, lo, hi);
+    x.m0 = r / tiles_n * 256;
+    x.n0 = r % tiles_n * BN;
+    x.k0 = uniform(lo);
+    rows(x, uniform(hi - lo));
+    return true;
+  }
+  SHP_DEV static void rows(Tile& x, int len) {
+    x.len = len;
+    x.kb = (len + BK - 1) / BK;
+    x.tail = len % BK;
+    x.tail_at = x.tail == 0 ? -1 : max(0, x.kb - 1 - TAIL_EARLY);
+  }
   SHP_DEV bool next(Tile& x) {
     if (first) {
       first = false;
       x = own;
       return true;
     }
-    if (!p.dynamic) return false;
-    const int t = feed.next();
-    if (t < 0) return false;
-    find(t, x);
-    return true;
-  }
-  SHP_DEV void find(int t, Tile& x) const {
-    const int i = t / per_e, r = t % per_e;
-    x.e = order != nullptr ? uniform(static_cast<int>(order[i])) : i;
-    int lo, hi;
-    p.g.range(x.e, lo, hi);
-    lo = uniform(lo);
-    hi = uniform(hi);
-    x.m0 = r / tiles_n * 256;
-    x.n0 = r % tiles_n * BN;
-    x.k0 = lo;
-    x.kb = (hi - lo + BK - 1) / BK;
-    x.tail = (hi - lo) % BK;
-    x.tail_at = x.tail == 0 ? -1 : max(0, x.kb - 1 - TAIL_EARLY);
+    int v[8];
+    feed.next(v);
+    x.e = v[0];
+    x.m0 = v[1];
+    x.n0 = v[2];
+    x.k0 = v[3];
+    rows(x, v[4]);
+    return x.e >= 0;
   }
 };
 
@@ -599,13 +600,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   Walk walk(p, sorted ? order : nullptr, slots, abort_flag);
   Tile x;
-  if (!sorted) walk.start();
+  const int turn = static_cast<int>(blockIdx.x) / 2;
+  if (!sorted) walk.find(turn, walk.own);
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // peer barriers initialised, both TMEM allocations done
   tc_fence_after();
   const uint32_t tmem = uniform(*tmem_slot);
-  if (sorted) walk.start();
+  if (sorted) walk.find(turn, walk.own);
   if (warp == 0) {
     // ---------------- TMA producer (both CTAs)
     const uint32_t on = elect_one(), lead = on & (leader ? 1u : 0u);
@@ -781,7 +783,19 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else if (warp == 2 + EPI_WARPS + 1) {
     // ---------------- scheduler (leader)
-    if (leader && p.dynamic && lane == 0) schedule_tiles(slots, INT32_MAX, abort_flag);
+    if (leader)
+      schedule_tiles(
+          slots, p.dynamic != 0, turn, static_cast<int>(gridDim.x) / 2,
+          [&](int t, int(&v)[8]) {
+            if (!walk.find(t, x)) return false;
+            v[0] = x.e;
+            v[1] = x.m0;
+            v[2] = x.n0;
+            v[3] = x.k0;
+            v[4] = x.len;
+            return true;
+          },
+          abort_flag);
   } else {
     // ---------------- clearing warp: rows behind the group in its last stage
     int kit = 0;

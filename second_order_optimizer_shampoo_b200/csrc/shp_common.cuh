@@ -420,18 +420,21 @@ SHP_DEV void mma_commit_pair_if(uint32_t on, uint32_t bar, uint16_t mask) {
 }
 
 // ------------------------------------------------- dynamic tile scheduling
-// A grid of one cluster (CTA pair) per tile, of which only those that fit run:
-// a running pair that wants another tile cancels the launch of a waiting one
-// and does that one's work (cluster launch control).  The hardware hands tiles
-// out as pairs become free, with no counter in memory to clear or to share
-// between launches.  A scheduler warp of the leader CTA asks, and passes the
-// tile's number to the roles of both CTAs through two slots.
+// A scheduler warp of a pair's leader CTA finds the pair's next tile and passes
+// its description (eight integers, the first >= 0) to the roles of both CTAs
+// through two slots, so that looking a tile up runs ahead of the work.
+//
+// Where tiles are handed out, the grid has one cluster (CTA pair) per tile, of
+// which only those that fit run: a running pair that wants another tile cancels
+// the launch of a waiting one and does that one's work (cluster launch
+// control).  The hardware hands tiles out as pairs become free, with no counter
+// in memory to clear or to share between launches.
 struct TileSlots {
   uint64_t full[2];   // per CTA: the slot holds a tile (or -1: no more)
   uint64_t empty[2];  // leader: every consumer of both CTAs has read it
   uint64_t asked;     // leader: the answer has arrived
   alignas(16) uint4 answer;
-  int tile[2];
+  alignas(16) int tile[2][8];
 };
 
 // Asks for another cluster; 16 bytes arrive in `answer`, counted on `bar`.
@@ -455,14 +458,18 @@ SHP_DEV int cancelled_cta(uint32_t answer) {
       : "memory");
   return x;
 }
-// Stores v in a CTA's shared memory (cluster address), 4 bytes counted on its
+// Stores a tile in a CTA's slot (cluster address), 32 bytes counted on its
 // barrier, on which this thread also arrives.
-SHP_DEV void slot_store(uint32_t addr, int v, uint32_t bar) {
-  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], 4;" ::"r"(bar)
+SHP_DEV void slot_store(uint32_t addr, const int (&v)[8], uint32_t bar) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], 32;" ::"r"(bar)
                : "memory");
-  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr),
-               "r"(v), "r"(bar)
-               : "memory");
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+            addr + 16u * i),
+        "r"(v[4 * i]), "r"(v[4 * i + 1]), "r"(v[4 * i + 2]), "r"(v[4 * i + 3]), "r"(bar)
+        : "memory");
 }
 
 SHP_DEV void tile_slots_init(TileSlots* ts, int consumers) {
@@ -473,44 +480,60 @@ SHP_DEV void tile_slots_init(TileSlots* ts, int consumers) {
   mbar_init(&ts->asked, 1);
 }
 
-// The scheduler, one thread of the leader.  Tiles from `limit` on hold no work
-// (a grid sized by an upper bound): they are cancelled and not passed on.
-// Every wait is bounded.
-SHP_DEV void schedule_tiles(TileSlots* ts, int limit, volatile int* abort_flag) {
+// The scheduler, a whole warp of the leader.  Tiles come from the launch's
+// waiting clusters (handed_out) or are every `step`-th from `t`.  find(t, v)
+// describes tile t, or is false if there is no such tile: then none follows it
+// in turn, and of those handed out (a grid sized by an upper bound) it is
+// dropped.  Every wait is bounded.
+template <class Find>
+SHP_DEV void schedule_tiles(TileSlots* ts, bool handed_out, int t, int step, Find find,
+                            volatile int* abort_flag) {
+  const int lane = threadIdx.x & 31;
   RingPos<2> at;
   uint32_t asked = 0;
   for (;;) {
-    if (!ring_wait(smem_u32(&ts->empty[at.slot]), at.parity ^ 1u, abort_flag)) return;
-    int cta;
-    do {
-      mbar_arrive_expect_tx(&ts->asked, 16);
-      try_cancel_cluster(smem_u32(&ts->answer), smem_u32(&ts->asked));
-      if (!ring_wait(smem_u32(&ts->asked), asked, abort_flag)) return;
-      asked ^= 1u;
-      cta = cancelled_cta(smem_u32(&ts->answer));
-      fence_proxy_async_smem();  // read before the next answer is written
-    } while (cta >= 0 && cta / 2 >= limit);
-    for (uint32_t r = 0; r < 2; ++r)
-      slot_store(mapa_shared(smem_u32(&ts->tile[at.slot]), r), cta < 0 ? -1 : cta / 2,
-                 mapa_shared(smem_u32(&ts->full[at.slot]), r));
-    if (cta < 0) return;
+    if (!warp_wait(smem_u32(&ts->empty[at.slot]), at.parity ^ 1u, abort_flag)) return;
+    int v[8] = {-1, 0, 0, 0, 0, 0, 0, 0};
+    if (handed_out) {
+      do {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&ts->asked, 16);
+          try_cancel_cluster(smem_u32(&ts->answer), smem_u32(&ts->asked));
+        }
+        if (!warp_wait(smem_u32(&ts->asked), asked, abort_flag)) return;
+        asked ^= 1u;
+        t = cancelled_cta(smem_u32(&ts->answer));
+        fence_proxy_async_smem();  // read before the next answer is written
+        t = uniform(t);
+        __syncwarp();
+      } while (t >= 0 && !find(t / 2, v));
+    } else {
+      t += step;
+      if (!find(t, v)) t = -1;
+    }
+    if (t < 0) v[0] = -1;
+    if (lane < 2)
+      slot_store(mapa_shared(smem_u32(ts->tile[at.slot]), lane), v,
+                 mapa_shared(smem_u32(&ts->full[at.slot]), lane));
+    if (t < 0) return;
     at.advance();
   }
 }
 
-// A consumer warp's view: next() gives the following tile's number to every
-// lane, or -1 when there is none left (or a wait gave up).
+// A consumer warp's view: next() gives the following tile's description to every
+// lane, v[0] = -1 when there is none left (or a wait gave up).
 struct TileFeed {
   TileSlots* ts;
   volatile int* abort_flag;
   RingPos<2> at;
-  SHP_DEV int next() {
-    if (!warp_wait(smem_u32(&ts->full[at.slot]), at.parity, abort_flag)) return -1;
-    const int t = uniform(*const_cast<volatile int*>(&ts->tile[at.slot]));
+  SHP_DEV void next(int (&v)[8]) {
+    v[0] = -1;
+    if (!warp_wait(smem_u32(&ts->full[at.slot]), at.parity, abort_flag)) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = uniform(const_cast<volatile int*>(ts->tile[at.slot])[i]);
     if ((threadIdx.x & 31) == 0)
       mbar_arrive_relaxed(mapa_shared(smem_u32(&ts->empty[at.slot]), 0));
     at.advance();
-    return t;
   }
 };
 
