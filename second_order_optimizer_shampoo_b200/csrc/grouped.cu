@@ -65,53 +65,29 @@ struct Groups {
   }
 };
 
-constexpr int SORT_MAX = 256;  // groups that are put in order (each thread compares all)
-
-// order[i] = the group of the i-th largest size (ties by number).  Called by all
-// threads of a block of at least SORT_MAX; `len` is scratch in shared memory.
-SHP_DEV void sort_groups(const Groups& g, uint16_t* order, int* len) {
-  const int e = static_cast<int>(threadIdx.x);
-  if (e < g.n) {
-    int lo, hi;
-    g.range(e, lo, hi);
-    len[e] = hi - lo;
-  }
-  __syncthreads();
-  if (e < g.n) {
-    int rank = 0;
-    for (int j = 0; j < g.n; ++j) rank += len[j] > len[e] || (len[j] == len[e] && j < e);
-    order[rank] = static_cast<uint16_t>(e);
-  }
-}
-
 // A tile of the rows product: `count` rows from row t0 in group e, weight
 // columns from n0.
 struct RowTile {
   int e, t0, count, n0;
 };
 
-// Looks row tiles up by number.  Tiles are numbered over the groups in order (by
-// falling size where sorted); a group of len rows has ceil(len / NT) row tiles
-// of equal size (up to the MMA's granule of 16), each with every column tile.
-// find() is called by whole warps and looks at 32 groups per step.
+// Looks row tiles up by number.  Tiles are numbered over the groups in order; a
+// group of len rows has ceil(len / NT) row tiles of equal size (up to the MMA's
+// granule of 16), each with every column tile.  find() is called by whole warps
+// and looks at 32 groups per step.
 template <int NT>
 struct RowTiles {
   const Groups g;
-  const uint16_t* order;  // null: the groups in their own order
   const int tiles_n;
   int e0 = 0;    // first group of the window
   int base = 0;  // tiles before the window
-  SHP_DEV RowTiles(const Groups& groups, int N, const uint16_t* o)
-      : g(groups), order(o), tiles_n((N + 255) / 256) {}
+  SHP_DEV RowTiles(const Groups& groups, int N) : g(groups), tiles_n((N + 255) / 256) {}
   SHP_DEV bool find(int t, RowTile& x) {
     if (t < base) e0 = base = 0;
     const int lane = threadIdx.x & 31;
     while (e0 < g.n) {
-      int a = 0, b = 0, e = e0 + lane;
-      if (e < g.n) {
-        if (order != nullptr) e = order[e];
-        g.range(e, a, b);
-      }
+      int a = 0, b = 0;
+      if (e0 + lane < g.n) g.range(e0 + lane, a, b);
       const int cnt = (b - a + NT - 1) / NT * tiles_n;
       int inc = cnt;
 #pragma unroll
@@ -126,7 +102,7 @@ struct RowTiles {
         const int lo = __shfl_sync(0xffffffffu, a, src), hi = __shfl_sync(0xffffffffu, b, src);
         const int tiles = (hi - lo + NT - 1) / NT;
         const int per = ((hi - lo + tiles - 1) / tiles + 15) & ~15;  // <= NT
-        x.e = uniform(__shfl_sync(0xffffffffu, e, src));
+        x.e = uniform(e0 + src);
         x.t0 = uniform(lo + r / tiles_n * per);
         x.count = uniform(min(per, hi - x.t0));
         x.n0 = uniform(r % tiles_n * 256);
@@ -181,7 +157,7 @@ struct RowsParams {
   Groups g;
   int N, K;
   int w_chunks;  // W [K][N] is mapped as 64-column chunks: both of a CTA in one box
-  int dynamic;   // tiles are handed out, the largest groups' first; else taken in turn
+  int dynamic;   // tiles are handed out; else taken in turn
   void* out;
 };
 
@@ -190,7 +166,7 @@ struct RowsCfg {
   static constexpr int X_BYTES = NT / 2 * 128;
   static constexpr int STAGE = A_BYTES + X_BYTES;
   static constexpr int BOXES = F32 ? EPI_WARPS * EPI_BOX : 0;
-  static constexpr int TAIL = BOXES + 320 + static_cast<int>(sizeof(TileSlots)) + SORT_MAX * 2;
+  static constexpr int TAIL = BOXES + 320 + static_cast<int>(sizeof(TileSlots));
   static constexpr int STAGES = (232448 - 1024 - TAIL) / STAGE;
   static constexpr int SMEM = 1024 + STAGES * STAGE + TAIL;
   static constexpr int THREADS = 32 * (2 + EPI_WARPS + 1);
@@ -220,9 +196,7 @@ __global__ void __launch_bounds__(RowsCfg<NT, F32>::THREADS, 1)
   uint64_t* drain = acce + 2;  // all MMAs of this pair complete
   volatile int* abort_flag = reinterpret_cast<volatile int*>(drain + 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1) + 1;
-  uint16_t* order = reinterpret_cast<uint16_t*>(drain + 2);
   static_assert((2 * STAGES + 5) * 8 + 8 <= 320, "barriers");
-  const bool sorted = p.dynamic && p.g.n <= SORT_MAX;
 
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -245,21 +219,16 @@ __global__ void __launch_bounds__(RowsCfg<NT, F32>::THREADS, 1)
     if (F32) tma_prefetch_desc(&tY);
   }
   if (warp == 1) tmem_alloc_pair(tmem_slot, 2 * NT);
-  if (sorted) {
-    sort_groups(p.g, order, reinterpret_cast<int*>(smem));
-    fence_proxy_async_smem();  // before the copies that reuse the space
-  }
-  RowTiles<NT> tiles(p.g, p.N, sorted ? order : nullptr);
+  RowTiles<NT> tiles(p.g, p.N);
   RowWalk walk(slots, abort_flag);
   RowTile x;
   const int turn = static_cast<int>(blockIdx.x) / 2;
-  if (!sorted) walk.have = tiles.find(turn, walk.own);
+  walk.have = tiles.find(turn, walk.own);
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // peer barriers initialised, both TMEM allocations done
   tc_fence_after();
   const uint32_t tmem = uniform(*tmem_slot);
-  if (sorted) walk.have = tiles.find(turn, walk.own);
   if (warp == 0) {
     // ---------------- TMA producer (both CTAs): its 128 columns of W and its
     // half of the tile's rows, in boxes of 32
@@ -470,14 +439,35 @@ __global__ void __launch_bounds__(RowsCfg<NT, F32>::THREADS, 1)
 //
 // k_grouped_wgrad: 256 x 256 tiles of G_e, both operands MN-major (rows of A
 // and B are the contraction), a 128-column half of each per CTA.  A tile's time
-// follows its group's rows, so tiles are handed out as pairs become free, the
-// largest groups' first: for 16 groups of 0.3 to 13 thousand rows the busiest
-// pair has 1 % more stages than the mean, in a fixed rotation 10 %.
+// follows its group's rows, so tiles are handed out as pairs become free, and
+// where they are long the largest groups' first: for 16 groups of 0.3 to 13
+// thousand rows the busiest pair has 1 % more stages than the mean, in a fixed
+// rotation 10 %.
 
 constexpr int STAGE_BYTES = 2 * A_BYTES;
 constexpr int STAGES = 6;
 constexpr int BN = 256;
 constexpr int THREADS = 32 * (2 + EPI_WARPS + 2);
+
+constexpr int SORT_MAX = 256;  // groups that are put in order (each thread compares all)
+
+// order[i] = the group of the i-th largest size (ties by number).  Called by all
+// threads of a block of at least SORT_MAX; `len` is scratch in shared memory.
+SHP_DEV void sort_groups(const Groups& g, uint16_t* order, int* len) {
+  const int e = static_cast<int>(threadIdx.x);
+  if (e < g.n) {
+    int lo, hi;
+    g.range(e, lo, hi);
+    len[e] = hi - lo;
+  }
+  __syncthreads();
+  if (e < g.n) {
+    int rank = 0;
+    for (int j = 0; j < g.n; ++j) rank += len[j] > len[e] || (len[j] == len[e] && j < e);
+    order[rank] = static_cast<uint16_t>(e);
+  }
+}
+
 constexpr int GSMEM = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * EPI_BOX + 320 +
                       static_cast<int>(sizeof(TileSlots)) + SORT_MAX * 2;
 static_assert(GSMEM <= 232448, "weight-gradient kernel exceeds shared memory");
@@ -487,7 +477,8 @@ struct WgradParams {
   int M, N;
   int accumulate;
   int chunks;   // A and B are mapped as 64-column chunks: both of a CTA in one box
-  int dynamic;  // more tiles than pairs: they are handed out
+  int sorted;   // the largest groups' tiles first
+  int dynamic;  // tiles are handed out; else taken in turn
 };
 
 // One tile: group e, tile (m0, n0), kb stages from row k0; `tail` valid rows in
@@ -570,7 +561,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(drain + 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1) + 1;
   uint16_t* order = reinterpret_cast<uint16_t*>(drain + 2);
-  const bool sorted = p.dynamic && p.g.n <= SORT_MAX;
+  const bool sorted = p.sorted != 0;
 
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -862,10 +853,12 @@ cudaError_t launch_rows(const CUtensorMap& w, const CUtensorMap& x, const CUtens
   if (li.err != cudaSuccess) return li.err;
   // every group with rows has at most one row tile more than its full ones
   const int64_t tiles = (T / NT + static_cast<int64_t>(p.g.n < T ? p.g.n : T)) * ((p.N + 255) / 256);
-  // Handing tiles out pays where their rows, and so their times, differ: 16
-  // skewed groups of about 192 rows, 4096 x 1024, 52 us against 76 in turn.  Few
-  // rows per group cost the same everywhere, and putting the groups in order is
-  // in the way: 16 rows over 64 groups, 1024 x 4096, 26.4 us against 25.6.
+  // Handing tiles out pays where their rows, and so their times, differ: 16384
+  // rows over 32 skewed groups, 512 x 2048, 44 us against 50 in turn (equal
+  // groups: 47 and 46).  Few rows per group cost the same everywhere, and asking
+  // for tiles is in the way: 16 rows over 64 groups, 1024 x 4096, 26.4 us
+  // against 25.6.  (Largest groups first, as in the weight gradient, did not
+  // pay here: 46 us.)
   const int64_t pairs = li.sms / 2;
   p.dynamic = tiles > pairs && T > 32 * static_cast<int64_t>(p.g.n) ? 1 : 0;
   cudaLaunchAttribute attr;
@@ -977,9 +970,16 @@ cudaError_t grouped_wgrad(const void* A, const void* B, const int64_t* offsets, 
   static std::atomic<uint64_t> done{0};
   const LaunchInfo li = launch_info(reinterpret_cast<const void*>(k_grouped_wgrad), GSMEM, done);
   if (li.err != cudaSuccess) return li.err;
-  p.dynamic = tiles > li.sms / 2 ? 1 : 0;
+  const int64_t pairs = li.sms / 2;
+  p.dynamic = tiles > pairs ? 1 : 0;
+  // Largest groups first ends even (16 skewed groups of about 4096 rows, 4096 x
+  // 1024: 421 us against 450), but puts the tiles that are all MMAs before those
+  // that are all stores: with few rows per tile mixing them is better (64 skewed
+  // groups of about 256 rows, 1024^2: 86 us sorted, 81 not; of 128 rows, 1024 x
+  // 4096: 241 and 229; from about 512 rows on, 43 and 52).
+  p.sorted = p.dynamic && groups <= SORT_MAX && T >= 512 * static_cast<int64_t>(groups) ? 1 : 0;
   cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = pair_grid(tiles, THREADS, GSMEM, st, &attr);
+  const cudaLaunchConfig_t cfg = pair_grid(p.dynamic || tiles < pairs ? tiles : pairs, THREADS, GSMEM, st, &attr);
   return cudaLaunchKernelEx(&cfg, k_grouped_wgrad, a, b, o, p);
 }
 
