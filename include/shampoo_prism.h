@@ -448,6 +448,12 @@ int prism_alpha_fit_noalloc(const float* R, int64_t n, int64_t batch, const floa
  *                        the loops use it when the batch's R fits in shared
  *                        memory): its first grid barrier, which CTA 0 never
  *                        reaches; no alpha is solved
+ *   SHP_SELFTEST_GROUPED, SHP_SELFTEST_WGRAD, SHP_SELFTEST_MX4_MATMUL  the
+ *                        grouped and 4-bit products: the MMA warp's first wait
+ *                        in both CTAs of the pair, with the producers' copies
+ *                        in flight (they are waited for)
+ *   SHP_SELFTEST_MX4_QUANTIZE  the 4-bit quantiser: the consumers' first wait,
+ *                        with the producer's copies in flight
  * status: one device int32, set to SHP_ETIMEOUT by the kernel (cleared
  * first).  alpha_out: one device float (may be NULL), for the sketch cases
  * the fit's alpha, which must come out NaN (no fit on incomplete vectors; the
@@ -459,6 +465,10 @@ int prism_alpha_fit_noalloc(const float* R, int64_t n, int64_t batch, const floa
 #define SHP_SELFTEST_SKETCH 2
 #define SHP_SELFTEST_SKETCH_ALPHA 3
 #define SHP_SELFTEST_SKETCH_CHAIN 4
+#define SHP_SELFTEST_GROUPED 5
+#define SHP_SELFTEST_WGRAD 6
+#define SHP_SELFTEST_MX4_QUANTIZE 7
+#define SHP_SELFTEST_MX4_MATMUL 8
 #define SHP_SELFTEST_WS_BYTES (4u << 20)
 int shp_selftest_bounded_wait(int which, int32_t* status, float* alpha_out, void* ws,
                               size_t ws_bytes, shp_stream stream);

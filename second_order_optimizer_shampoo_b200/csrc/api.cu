@@ -977,7 +977,9 @@ int shp_selftest_bounded_wait(int which, int32_t* status, float* alpha_out, void
                               size_t ws_bytes, shp_stream stream) {
   if (status == nullptr || ws == nullptr || ws_bytes < SHP_SELFTEST_WS_BYTES) return SHP_EINVAL;
   if (which != SHP_SELFTEST_GEMM && which != SHP_SELFTEST_OZAKI && which != SHP_SELFTEST_SKETCH &&
-      which != SHP_SELFTEST_SKETCH_ALPHA && which != SHP_SELFTEST_SKETCH_CHAIN)
+      which != SHP_SELFTEST_SKETCH_ALPHA && which != SHP_SELFTEST_SKETCH_CHAIN &&
+      which != SHP_SELFTEST_GROUPED && which != SHP_SELFTEST_WGRAD &&
+      which != SHP_SELFTEST_MX4_QUANTIZE && which != SHP_SELFTEST_MX4_MATMUL)
     return SHP_EINVAL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   CK(cudaMemsetAsync(status, 0, sizeof(int32_t), st));
@@ -993,6 +995,25 @@ int shp_selftest_bounded_wait(int which, int32_t* status, float* alpha_out, void
     e.selftest = 1;
     CK(gemm_tc(MODE_TF32, op(A, nullptr, false, n, n * n), op(B, nullptr, true, n, n * n), n, n,
                n, 1, e, st));
+  } else if (which == SHP_SELFTEST_GROUPED || which == SHP_SELFTEST_WGRAD) {
+    // one group of 200 rows (its last stage is partial), one tile
+    int64_t* off = a.take<int64_t>(2);
+    uint16_t* A = a.take<uint16_t>(n * n);
+    uint16_t* B = a.take<uint16_t>(n * n);
+    float* C = a.take<float>(n * n);
+    CK(cudaMemsetAsync(off + 1, 200, 1, st));  // offsets {0, 200}, little-endian
+    if (which == SHP_SELFTEST_GROUPED)
+      CK(grouped_rows(A, off, B, false, C, 200, n, n, 1, true, st, status));
+    else
+      CK(grouped_wgrad(A, B, off, C, 200, n, n, 1, false, st, status));
+  } else if (which == SHP_SELFTEST_MX4_QUANTIZE) {
+    uint8_t* Q = a.take<uint8_t>(shp_mx4_code_bytes(n, n, 1));
+    uint8_t* S = a.take<uint8_t>(shp_mx4_scale_bytes(n, n, 1));
+    CK(mx4_quantize(a.take<float>(n * n), false, n, n, 1, Q, S, nullptr, nullptr, st, status));
+  } else if (which == SHP_SELFTEST_MX4_MATMUL) {
+    uint8_t* Q = a.take<uint8_t>(shp_mx4_code_bytes(n, 4 * n, 1));
+    uint8_t* S = a.take<uint8_t>(shp_mx4_scale_bytes(n, 4 * n, 1));
+    CK(mx4_gemm(Q, S, Q, S, a.take<float>(n * n), true, n, n, 4 * n, 1, st, status));
   } else if (which == SHP_SELFTEST_OZAKI) {
     const OzSlices sa = carve_slices(a, n, n, 1, true, false);
     const OzSlices sb = carve_slices(a, n, n, 1, false, true);

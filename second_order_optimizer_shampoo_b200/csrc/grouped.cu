@@ -6,12 +6,12 @@
 //   wgrad     G_e   = A_e^T B_e (+ G_e),  A_e, B_e the rows [off_e, off_{e+1})
 //
 // bf16 operands, fp32 accumulation.  The group boundaries are read on the
-// device, so nothing waits for the host.  k_grouped is a persistent CTA-pair
-// kernel (one tcgen05 MMA of M = 256 over two SMs, 256 x 256 tiles, TMA ring,
-// two TMEM accumulators so that the epilogue of one tile runs beside the main
-// loop of the next), like the batched product of gemm_tc.cu; what differs is
-// where tiles come from (a warp-wide scan of the offsets), the ragged edges,
-// and the fp32 sums:
+// device, so nothing waits for the host.  Both kernels are persistent CTA-pair
+// kernels (one tcgen05 MMA of M = 256 over two SMs, tiles up to 256 x 256, TMA
+// ring, two TMEM accumulators so that the epilogue of one tile runs beside the
+// main loop of the next), like the batched product of gemm_tc.cu; what differs
+// is where tiles come from (a scheduler warp that scans the offsets), the ragged
+// edges, and the fp32 sums:
 //   - row tiles start at any row; rows of the next group that a tile's box
 //     also holds are multiplied but not stored (a row of Y depends on its own
 //     row of X alone);
@@ -48,7 +48,6 @@ SHP_DEV void tma_reduce_add_3d(const CUtensorMap* map, const void* src, int x, i
       "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
-
 
 // Group e covers the rows [lo, hi): the offsets clamped to 0..T and to
 // non-negative lengths, so that no offset array reaches outside the operands.
@@ -153,12 +152,18 @@ struct RowWalk {
 // (stored directly, 4 bytes per lane, a 256 x 256 tile took 9700 clocks of
 // stores, more than the MMAs of K = 1024: 65536 rows x 1024 x 4096 590 us, now 481),
 // partial ones directly.
+//
+// Bound and rate: tensor pipe for long groups (65536 rows over 16 groups, 4096 x
+// 1024: 368 us = 1494 TFLOP/s in a short run, 533 clocks per stage of 512), HBM
+// for short ones (64 rows over 64 groups, 1024 x 4096: 45.7 us for 280 MB of W =
+// 6.1 TB/s).
 struct RowsParams {
   Groups g;
   int N, K;
   int w_chunks;  // W [K][N] is mapped as 64-column chunks: both of a CTA in one box
   int dynamic;   // tiles are handed out; else taken in turn
   void* out;
+  int* status;   // bounded-wait self-test: receives SHP_ETIMEOUT (else null)
 };
 
 template <int NT, bool F32>
@@ -194,9 +199,10 @@ __global__ void __launch_bounds__(RowsCfg<NT, F32>::THREADS, 1)
   uint64_t* accf = empty + STAGES;
   uint64_t* acce = accf + 2;
   uint64_t* drain = acce + 2;  // all MMAs of this pair complete
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(drain + 1);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1) + 1;
-  static_assert((2 * STAGES + 5) * 8 + 8 <= 320, "barriers");
+  uint64_t* never = drain + 1;  // completed by nothing: the self-test's wait
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(never + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1) + 1;
+  static_assert((2 * STAGES + 6) * 8 + 8 <= 320, "barriers");
 
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -209,6 +215,7 @@ __global__ void __launch_bounds__(RowsCfg<NT, F32>::THREADS, 1)
       mbar_init(&acce[u], 2 * EPI_WARPS);
     }
     mbar_init(drain, 1);
+    mbar_init(never, 1);
     // consumers: producer and epilogue warps of both CTAs, MMA warp
     tile_slots_init(slots, 2 * (EPI_WARPS + 1) + 1);
     *abort_flag = 0;
@@ -236,6 +243,7 @@ __global__ void __launch_bounds__(RowsCfg<NT, F32>::THREADS, 1)
     RingPos<STAGES> ring;
     const uint32_t stages = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty);
     const uint32_t fleader = uniform(mapa_shared(full0, 0));
+    int landing = 0;  // an abort flag of its own for the last wait
     bool stop = false;
     while (!stop && walk.next(x)) {
       const int n0 = x.n0 + static_cast<int>(rank) * 128;
@@ -270,12 +278,14 @@ __global__ void __launch_bounds__(RowsCfg<NT, F32>::THREADS, 1)
         ring.advance();
       }
     }
-    // a wait that gave up leaves copies in flight that no MMA waits for: let
-    // them land (bounded) before the CTAs exit
-    if (stop && leader) {
-      for (int k = 0; k < STAGES; ++k, ring.advance()) mbar_wait(&full[ring.slot], ring.parity ^ 1u);
+    // no copy may be in flight when the CTAs exit, also where a wait gave up and
+    // no MMA waits for it (the leader's barriers count the peer's copies too)
+    if (leader) {
+      for (int k = 0; k < STAGES; ++k, ring.advance())
+        ring_wait(full0 + ring.slot * 8, ring.parity ^ 1u, &landing);
     }
   } else if (warp == 1) {
+    const bool gave_up = selftest_wait(p.status, never, abort_flag);
     if (leader) {
       // ---------------- MMA issuer (leader of the pair)
       const uint32_t on = elect_one();
@@ -287,7 +297,7 @@ __global__ void __launch_bounds__(RowsCfg<NT, F32>::THREADS, 1)
                                   : smem_desc(smem_u32(smem), 16, 1024u, 2u);
       const uint64_t xdesc = smem_desc(smem_u32(smem) + A_BYTES, 16, 1024u, 2u);
       constexpr uint64_t WSTEP = (W_MN ? 16 * 128 : 32) >> 4, XSTEP = 32 >> 4;
-      bool stop = false;
+      bool stop = gave_up;
       while (!stop && walk.next(x)) {
         const uint32_t idesc = instr_desc(1u, W_MN, false, 256, (x.count + 15) & ~15);
         for (int c0 = 0; c0 < KB && !stop; c0 += F32 ? CHUNK_KB : KB, au.advance()) {
@@ -427,7 +437,8 @@ __global__ void __launch_bounds__(RowsCfg<NT, F32>::THREADS, 1)
     }
   }
 
-  if (warp == 1) mbar_wait(drain, 0);  // bounded; immediate unless a wait above gave up
+  // every MMA has completed (bounded; suspended, as the peer's warp waits all along)
+  if (warp == 1) warp_wait(smem_u32(drain), 0, abort_flag);
   tc_fence_before();
   __syncthreads();
   // releasing: this CTA's arrivals on the other's barriers land before it exits
@@ -443,6 +454,9 @@ __global__ void __launch_bounds__(RowsCfg<NT, F32>::THREADS, 1)
 // where they are long the largest groups' first: for 16 groups of 0.3 to 13
 // thousand rows the busiest pair has 1 % more stages than the mean, in a fixed
 // rotation 10 %.
+// Bound and rate: tensor pipe for long groups (that case, 1024 x 4096,
+// accumulated: 422 us = 1303 TFLOP/s in a short run), the stores of G for short
+// ones (64 groups of 256 rows, 1024^2: 64 us for 335 MB = 5.2 TB/s).
 
 constexpr int STAGE_BYTES = 2 * A_BYTES;
 constexpr int STAGES = 6;
@@ -479,6 +493,7 @@ struct WgradParams {
   int chunks;   // A and B are mapped as 64-column chunks: both of a CTA in one box
   int sorted;   // the largest groups' tiles first
   int dynamic;  // tiles are handed out; else taken in turn
+  int* status;  // bounded-wait self-test: receives SHP_ETIMEOUT (else null)
 };
 
 // One tile: group e, tile (m0, n0), kb stages from row k0; `tail` valid rows in
@@ -558,9 +573,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* tailb = acce + 2;        // per stage: a partial stage of this CTA has landed
   uint64_t* clearb = tailb + STAGES;  // per stage (leader): the peer's half is cleared
   uint64_t* drain = clearb + STAGES;  // all MMAs of this pair complete
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(drain + 1);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1) + 1;
-  uint16_t* order = reinterpret_cast<uint16_t*>(drain + 2);
+  uint64_t* never = drain + 1;        // completed by nothing: the self-test's wait
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(never + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1) + 1;
+  uint16_t* order = reinterpret_cast<uint16_t*>(never + 2);
+  static_assert((4 * STAGES + 6) * 8 + 8 <= 320, "barriers");
   const bool sorted = p.sorted != 0;
 
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
@@ -576,6 +593,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(&acce[u], 2 * EPI_WARPS);
     }
     mbar_init(drain, 1);
+    mbar_init(never, 1);
     // consumers: producer, epilogue and clearing warps of both CTAs, MMA warp
     tile_slots_init(slots, 2 * (EPI_WARPS + 2) + 1);
     *abort_flag = 0;
@@ -605,6 +623,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     RingPos<STAGES> ring;
     const uint32_t stages = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty);
     const uint32_t tail0 = smem_u32(tailb), fleader = uniform(mapa_shared(full0, 0));
+    int landing = 0;  // an abort flag of its own for the last wait
     bool stop = false;
     while (!stop && walk.next(x)) {
       const int m0 = x.m0 + static_cast<int>(rank) * 128;
@@ -647,12 +666,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         ring.advance();
       }
     }
-    // a wait that gave up leaves copies in flight that no MMA waits for: let
-    // them land (bounded) before the CTAs exit
-    if (stop && leader) {
-      for (int k = 0; k < STAGES; ++k, ring.advance()) mbar_wait(&full[ring.slot], ring.parity ^ 1u);
+    // no copy may be in flight when the CTAs exit, also where a wait gave up and
+    // no MMA waits for it (the leader's barriers count the peer's copies too)
+    if (leader) {
+      for (int k = 0; k < STAGES; ++k, ring.advance())
+        ring_wait(full0 + ring.slot * 8, ring.parity ^ 1u, &landing);
     }
   } else if (warp == 1) {
+    const bool gave_up = selftest_wait(p.status, never, abort_flag);
     if (leader) {
       // ---------------- MMA issuer (leader of the pair)
       const uint32_t idesc = instr_desc(1u, true, true, 256, BN);
@@ -664,7 +685,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint64_t adesc = smem_desc(smem_u32(smem), BK * 128, 1024u, 2u);
       const uint64_t bdesc = smem_desc(smem_u32(smem) + A_BYTES, BK * 128, 1024u, 2u);
       constexpr uint64_t KSTEP = 16 * 128 >> 4;
-      bool stop = false;
+      bool stop = gave_up;
       while (!stop && walk.next(x)) {
         int l = 0;                 // place in the order of loading
         RingPos<STAGES> tail = ring;  // where the partial stage is
@@ -718,57 +739,57 @@ __global__ void __launch_bounds__(THREADS, 1)
     while (!stop && walk.next(x)) {
       const int row0 = x.m0 + static_cast<int>(rank) * 128 + q * 32;
       const int c0 = x.n0 + h * 128;
-        float acc[128];
+      float acc[128];
 #pragma unroll
-        for (int j = 0; j < 128; ++j) acc[j] = 0.f;
-        const int nc = (x.kb + CHUNK_KB - 1) / CHUNK_KB;
-        for (int c = 0; c < nc; ++c, ++it) {
-          const int u = it & 1;
-          if (!warp_wait(smem_u32(&accf[u]), (it >> 1) & 1, abort_flag)) {
-            stop = true;
-            break;
-          }
-          tc_fence_after();
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            float v[32];
-            tmem_ld32(trow + static_cast<uint32_t>(u * BN + g * 32), v);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) acc[g * 32 + j] += v[j];
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_relaxed(mapa_shared(smem_u32(&acce[u]), 0));
+      for (int j = 0; j < 128; ++j) acc[j] = 0.f;
+      const int nc = (x.kb + CHUNK_KB - 1) / CHUNK_KB;
+      for (int c = 0; c < nc; ++c, ++it) {
+        const int u = it & 1;
+        if (!warp_wait(smem_u32(&accf[u]), (it >> 1) & 1, abort_flag)) {
+          stop = true;
+          break;
         }
-        if (stop) break;
-        if (p.accumulate && nc == 0) continue;  // an empty group leaves G as it is
-        if (row0 >= p.M) continue;
+        tc_fence_after();
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const int cb = c0 + g * 32;
-          if (cb >= p.N) continue;
-          // the warp's box, or, when no more tiles come, a box of its own for
-          // each store in the stages, which nothing reads or fills any more
-          uint8_t* bx = p.dynamic ? box : smem + ((warp - 2) * 4 + g) * EPI_BOX;
-          if (p.dynamic) {
-            if (lane == 0) bulk_wait_read_all();  // the last store has read the box
-            __syncwarp();
-          }
+          float v[32];
+          tmem_ld32(trow + static_cast<uint32_t>(u * BN + g * 32), v);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<float4*>(bx + sw128_off(lane, i)) =
-                make_float4(acc[g * 32 + 4 * i], acc[g * 32 + 4 * i + 1], acc[g * 32 + 4 * i + 2],
-                            acc[g * 32 + 4 * i + 3]);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if (p.accumulate)
-              tma_reduce_add_3d(&tO, bx, cb, row0, x.e);
-            else
-              tma_store_3d(&tO, bx, cb, row0, x.e);
-            bulk_commit();
-          }
+          for (int j = 0; j < 32; ++j) acc[g * 32 + j] += v[j];
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_relaxed(mapa_shared(smem_u32(&acce[u]), 0));
+      }
+      if (stop) break;
+      if (p.accumulate && nc == 0) continue;  // an empty group leaves G as it is
+      if (row0 >= p.M) continue;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int cb = c0 + g * 32;
+        if (cb >= p.N) continue;
+        // the warp's box, or, when no more tiles come, a box of its own for
+        // each store in the stages, which nothing reads or fills any more
+        uint8_t* bx = p.dynamic ? box : smem + ((warp - 2) * 4 + g) * EPI_BOX;
+        if (p.dynamic) {
+          if (lane == 0) bulk_wait_read_all();  // the last store has read the box
+          __syncwarp();
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<float4*>(bx + sw128_off(lane, i)) =
+              make_float4(acc[g * 32 + 4 * i], acc[g * 32 + 4 * i + 1], acc[g * 32 + 4 * i + 2],
+                          acc[g * 32 + 4 * i + 3]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (p.accumulate)
+            tma_reduce_add_3d(&tO, bx, cb, row0, x.e);
+          else
+            tma_store_3d(&tO, bx, cb, row0, x.e);
+          bulk_commit();
+        }
+      }
     }
     if (lane == 0) bulk_wait_all();  // nothing outlives the CTA's shared memory
     __syncwarp();
@@ -818,7 +839,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   }
 
-  if (warp == 1) mbar_wait(drain, 0);  // bounded; immediate unless a wait above gave up
+  // every MMA has completed (bounded; suspended, as the peer's warp waits all along)
+  if (warp == 1) warp_wait(smem_u32(drain), 0, abort_flag);
   tc_fence_before();
   __syncthreads();
   // releasing: this CTA's arrivals on the other's barriers land before it exits
@@ -914,13 +936,15 @@ int rows_per_tile(int64_t T, int64_t N, int64_t groups) {
 }  // namespace
 
 cudaError_t grouped_rows(const void* X, const int64_t* offsets, const void* W, bool w_trans,
-                         void* Y, int T, int K, int N, int groups, bool f32, cudaStream_t st) {
+                         void* Y, int T, int K, int N, int groups, bool f32, cudaStream_t st,
+                         int* selftest) {
   RowsParams p;
   memset(&p, 0, sizeof(p));
   p.g = Groups{offsets, groups, T};
   p.N = N;
   p.K = K;
   p.out = Y;
+  p.status = selftest;
   CUtensorMap w;
   const int64_t kn = static_cast<int64_t>(K) * N;
   bool ok;
@@ -942,7 +966,8 @@ cudaError_t grouped_rows(const void* X, const int64_t* offsets, const void* W, b
 }
 
 cudaError_t grouped_wgrad(const void* A, const void* B, const int64_t* offsets, float* G, int T,
-                          int M, int N, int groups, bool accumulate, cudaStream_t st) {
+                          int M, int N, int groups, bool accumulate, cudaStream_t st,
+                          int* selftest) {
   WgradParams p;
   memset(&p, 0, sizeof(p));
   CUtensorMap a, b, o;
@@ -966,6 +991,7 @@ cudaError_t grouped_wgrad(const void* A, const void* B, const int64_t* offsets, 
   p.M = M;
   p.N = N;
   p.accumulate = accumulate ? 1 : 0;
+  p.status = selftest;
   const int64_t tiles = static_cast<int64_t>(groups) * ((M + 255) / 256) * ((N + BN - 1) / BN);
   static std::atomic<uint64_t> done{0};
   const LaunchInfo li = launch_info(reinterpret_cast<const void*>(k_grouped_wgrad), GSMEM, done);
@@ -979,7 +1005,8 @@ cudaError_t grouped_wgrad(const void* A, const void* B, const int64_t* offsets, 
   // 4096: 241 and 229; from about 512 rows on, 43 and 52).
   p.sorted = p.dynamic && groups <= SORT_MAX && T >= 512 * static_cast<int64_t>(groups) ? 1 : 0;
   cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = pair_grid(p.dynamic || tiles < pairs ? tiles : pairs, THREADS, GSMEM, st, &attr);
+  const cudaLaunchConfig_t cfg =
+      pair_grid(p.dynamic || tiles < pairs ? tiles : pairs, THREADS, GSMEM, st, &attr);
   return cudaLaunchKernelEx(&cfg, k_grouped_wgrad, a, b, o, p);
 }
 

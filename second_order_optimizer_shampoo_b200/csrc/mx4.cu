@@ -74,7 +74,8 @@ SHP_DEV uint32_t quantize_block(float* x, uint32_t* q) {
 // stores (which clip the edge).  The tile stays in X's type, in boxes of
 // 128-byte rows with the 128-byte swizzle: a warp whose lanes own 32 rows
 // (16-byte reads) and one whose lanes own 32 columns both read it without bank
-// conflicts, so one copy serves both orientations.
+// conflicts, so one copy serves both orientations.  Bound by HBM: 16 x 4096 x
+// 1024 fp32 along both axes 60 us = 5.65 TB/s, along one 53 us = 5.76.
 constexpr int QTHREADS = 512;
 constexpr int QSTG = 2 * 8192 + 2 * 512;  // codes and scales of both orientations
 
@@ -86,9 +87,10 @@ struct QCfg {
 };
 
 struct QParams {
-  int rows, cols, tiles_r, tiles_c;
+  int tiles_r, tiles_c;
   int64_t tiles;
   uint8_t* s[2];  // scale tiles per orientation (null: not wanted)
+  int* status;    // bounded-wait self-test: receives SHP_ETIMEOUT (else null)
 };
 
 SHP_DEV void bulk_store(void* dst, const void* src, uint32_t bytes) {
@@ -110,8 +112,10 @@ __global__ void __launch_bounds__(QTHREADS + 32, 1)
   uint8_t* stg = smem + C::STAGES * C::TILE;
   uint64_t* full = reinterpret_cast<uint64_t*>(stg + QSTG);
   uint64_t* empty = full + C::STAGES;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + C::STAGES);
+  uint64_t* never = empty + C::STAGES;  // completed by nothing: the self-test's wait
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(never + 1);
   if (threadIdx.x == 0) {
+    mbar_init(never, 1);
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], QTHREADS / 32);
@@ -128,12 +132,7 @@ __global__ void __launch_bounds__(QTHREADS + 32, 1)
       int it = 0;
       for (int64_t t = blockIdx.x; t < p.tiles; t += gridDim.x, ++it) {
         const int s = it % C::STAGES;
-        if (it >= C::STAGES && !mbar_wait(&empty[s], ((it / C::STAGES) - 1) & 1)) {
-          // the consumers gave up: let the copies in flight land (bounded)
-          for (int i = it - C::STAGES; i < it; ++i)
-            mbar_wait(&full[i % C::STAGES], (i / C::STAGES) & 1);
-          break;
-        }
+        if (it >= C::STAGES && !mbar_wait(&empty[s], ((it / C::STAGES) - 1) & 1)) break;
         const int b = static_cast<int>(t / per_b), r = static_cast<int>(t % per_b);
         const int c0 = r % p.tiles_c * QT, r0 = r / p.tiles_c * QT;
         mbar_arrive_expect_tx(&full[s], C::TILE);
@@ -141,6 +140,10 @@ __global__ void __launch_bounds__(QTHREADS + 32, 1)
         for (int i = 0; i < QT / W; ++i)
           tma_load_3d(smem + s * C::TILE + i * QT * 128, &tX, &full[s], c0 + i * W, r0, b);
       }
+      // no copy may be in flight when the CTA exits, also where the consumers
+      // gave up and do not wait for it
+      for (int i = it > C::STAGES ? it - C::STAGES : 0; i < it; ++i)
+        mbar_wait(&full[i % C::STAGES], (i / C::STAGES) & 1);
     }
     return;
   }
@@ -151,6 +154,7 @@ __global__ void __launch_bounds__(QTHREADS + 32, 1)
     const uint8_t* tile = smem + s * C::TILE;
     // a wait that gives up is acted on behind the barrier below, by all warps
     // together (only consumers set the flag)
+    if (it == 0) selftest_wait(p.status, never, abort_flag);
     if (!mbar_wait(&full[s], (it / C::STAGES) & 1)) *abort_flag = 1;
     uint32_t q[2][4], sb[2];
     if (p.s[0] != nullptr) {
@@ -241,7 +245,8 @@ SHP_DEV void e2m1x2(uint32_t w, float& a, float& b) {
 // A CTA restores one 128 x 128 tile; a warp's store is one (fp32: 4 values per
 // lane) or two (bf16: 8 values per lane) contiguous row segments, and each
 // lane has eight loads of codes in flight.  Values are exact in either type
-// (one mantissa bit, exponents down to 2^-128).
+// (one mantissa bit, exponents down to 2^-128).  Bound by HBM: 16 x 4096 x 1024 to
+// fp32 54 us = 5.6 TB/s.
 template <bool BF16>
 __global__ void __launch_bounds__(256)
     k_mx4_dequantize(const uint8_t* Q, const uint8_t* S, int rows, int cols, int tiles_r,
@@ -334,6 +339,10 @@ __global__ void __launch_bounds__(256)
 //
 // fp32 results are summed in chunks of CHUNK_KB stages (32 MMAs) in the tensor
 // core, which adds with truncation, and over chunks in registers.
+//
+// Bound and rate: a stage brings 35 KB into each SM for 512 clocks of MMAs, 68
+// bytes per clock, about what the path from L2 delivers: 8192 x 8192 x 4096 97 us
+// = 5.67 PFLOP/s in a short run, 589 clocks per stage; under the power cap 119 us.
 
 constexpr int BN = 256;
 constexpr int MK = 256;            // codes per stage row: 128 bytes
@@ -387,7 +396,7 @@ struct Mx4Params {
   int tiles_m, tiles_n;
   int64_t batch;
   int rb_a, rb_b;  // 128-row scale tiles per matrix of A and B
-  void* out;
+  int* status;     // bounded-wait self-test: receives SHP_ETIMEOUT (else null)
 };
 
 template <bool F32>
@@ -412,8 +421,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* accf = empty + STAGES;  // accumulator u complete
   uint64_t* acce = accf + 2;        // shared columns drained, and all of the accumulator before
   uint64_t* drain = acce + 1;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(drain + 1);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1) + 1;
+  uint64_t* never = drain + 1;  // completed by nothing: the self-test's wait
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(never + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1) + 1;
 
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -425,6 +435,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init(&accf[1], 1);
     mbar_init(acce, 2 * EPI_WARPS);
     mbar_init(drain, 1);
+    mbar_init(never, 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tA);
@@ -469,13 +480,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         ring.advance();
       }
     }
-    // a wait that gave up leaves copies in flight that no MMA waits for: let
-    // them land (bounded) before the CTAs exit
-    if (stop && leader) {
+    // no copy may be in flight when the CTAs exit, also where a wait gave up and
+    // no MMA waits for it (the leader's barriers count the peer's copies too)
+    int landing = 0;  // an abort flag of its own for this wait
+    if (leader) {
       for (int k = 0; k < STAGES; ++k, ring.advance())
-        mbar_wait(&full[ring.slot], ring.parity ^ 1u);
+        ring_wait(full0 + ring.slot * 8, ring.parity ^ 1u, &landing);
     }
   } else if (warp == 1) {
+    const bool gave_up = selftest_wait(p.status, never, abort_flag);
     if (leader) {
       // ---------------- MMA issuer (leader of the pair)
       const uint32_t on = elect_one();
@@ -487,7 +500,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint64_t sdesc = smem_desc(smem_u32(smem) + 2 * TILE_BYTES, 128, 128, 0);
       uint32_t u = 0, pe = 1;  // accumulator; parity of acce's last use
       uint32_t sf = 0;         // scale buffer
-      bool stop = false;
+      bool stop = gave_up;
       for (int t = cl; t < ntiles && !stop; t += ncl) {
         for (int c0 = 0; c0 < KB && !stop; c0 += F32 ? CHUNK_KB : KB, u ^= 1u, pe ^= 1u) {
           const int c1 = F32 ? min(c0 + CHUNK_KB, KB) : KB;
@@ -631,7 +644,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
   }
 
-  if (warp == 1) mbar_wait(drain, 0);  // bounded; immediate unless a wait above gave up
+  // every MMA has completed (bounded; suspended, as the peer's warp waits all along)
+  if (warp == 1) warp_wait(smem_u32(drain), 0, abort_flag);
   tc_fence_before();
   __syncthreads();
   // releasing: this CTA's arrivals on the other's barriers land before it exits
@@ -662,10 +676,10 @@ cudaError_t launch_quantize(const CUtensorMap& x, const CUtensorMap& q, const CU
 }  // namespace
 
 cudaError_t mx4_quantize(const void* X, bool bf16, int rows, int cols, int64_t batch, uint8_t* Q,
-                         uint8_t* S, uint8_t* Qt, uint8_t* St, cudaStream_t st) {
+                         uint8_t* S, uint8_t* Qt, uint8_t* St, cudaStream_t st,
+                         int* selftest) {
   QParams p;
-  p.rows = rows;
-  p.cols = cols;
+  p.status = selftest;
   p.tiles_r = static_cast<int>(ceil_div(rows, QT));
   p.tiles_c = static_cast<int>(ceil_div(cols, QT));
   p.tiles = batch * p.tiles_r * p.tiles_c;
@@ -698,9 +712,11 @@ cudaError_t mx4_dequantize(const uint8_t* Q, const uint8_t* S, int rows, int col
 }
 
 cudaError_t mx4_gemm(const uint8_t* A, const uint8_t* As, const uint8_t* B, const uint8_t* Bs,
-                     void* C, bool f32, int M, int N, int K, int64_t batch, cudaStream_t st) {
+                     void* C, bool f32, int M, int N, int K, int64_t batch, cudaStream_t st,
+                     int* selftest) {
   Mx4Params p;
   memset(&p, 0, sizeof(p));
+  p.status = selftest;
   p.M = M;
   p.N = N;
   p.K = K;
@@ -709,7 +725,6 @@ cudaError_t mx4_gemm(const uint8_t* A, const uint8_t* As, const uint8_t* B, cons
   p.tiles_n = static_cast<int>(ceil_div(N, BN));
   p.rb_a = static_cast<int>(ceil_div(M, 128));
   p.rb_b = static_cast<int>(ceil_div(N, 128));
-  p.out = C;
   const int64_t kt = ceil_div(K, 128);
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n * batch;
   if (tiles > INT32_MAX / 2 || batch * p.rb_a > INT32_MAX || batch * p.rb_b > INT32_MAX)

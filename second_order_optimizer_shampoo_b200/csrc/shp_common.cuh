@@ -137,6 +137,16 @@ SHP_DEV bool warp_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abor
 // completes (about 10 ms): long enough to be a real wait, short for a test.
 #define SHP_SELFTEST_LIMIT (20000000LL)
 
+// Bounded-wait self-test of a kernel (status non-null): waits on a barrier that
+// nothing completes, records the timeout and raises the block's abort flag.
+// True if it did.
+SHP_DEV bool selftest_wait(int* status, uint64_t* never, volatile int* abort_flag) {
+  if (status == nullptr || mbar_wait(never, 0, nullptr, SHP_SELFTEST_LIMIT)) return false;
+  *abort_flag = 1;
+  atomicExch(status, 19);  // SHP_ETIMEOUT
+  return true;
+}
+
 SHP_DEV void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
