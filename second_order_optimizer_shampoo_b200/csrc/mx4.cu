@@ -5,7 +5,7 @@
 // scale 2^e, e = floor(log2 max|x_i|) - 2, kept as the byte e + 127; a value
 // is a 4-bit float (sign, 2 exponent bits, 1 mantissa bit: 0, .5, 1, 1.5, 2,
 // 3, 4, 6) of x_i / 2^e, rounded to nearest with ties to even and saturated
-// at 6 (so that max|x| in (7, 8) 2^e is clipped by up to a quarter).
+// at 6 (magnitudes in (6, 8) 2^e come out as 6 2^e).
 //
 // Layout: a matrix of R rows and C columns has rows of Cp / 2 bytes, Cp = C
 // rounded up to whole blocks, element 2j in the low nibble of byte j, zero
