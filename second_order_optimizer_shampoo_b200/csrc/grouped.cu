@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(RowsCfg<NT, F32>::THREADS, 1)
       const int boxes = (half + 31) / 32;
       const uint32_t tx = 2 * (A_BYTES + (small ? boxes * 4096u : C::X_BYTES));
       for (int k0 = 0; k0 < p.K; k0 += BK) {
-        if (!warp_wait(empty0 + ring.slot * 8, ring.parity ^ 1u, abort_flag)) {
+        if (!issue_wait(empty0 + ring.slot * 8, ring.parity ^ 1u, abort_flag)) {
           stop = true;
           break;
         }
@@ -302,14 +302,14 @@ __global__ void __launch_bounds__(RowsCfg<NT, F32>::THREADS, 1)
         const uint32_t idesc = instr_desc(1u, W_MN, false, 256, (x.count + 15) & ~15);
         for (int c0 = 0; c0 < KB && !stop; c0 += F32 ? CHUNK_KB : KB, au.advance()) {
           const int c1 = F32 ? min(c0 + CHUNK_KB, KB) : KB;
-          if (!warp_wait(acce0 + au.slot * 8, au.parity ^ 1u, abort_flag)) {
+          if (!issue_wait(acce0 + au.slot * 8, au.parity ^ 1u, abort_flag)) {
             stop = true;
             break;
           }
           tc_fence_after();
           const uint32_t dacc = tmem + au.slot * NT;
           for (int kb = c0; kb < c1; ++kb) {
-            if (!warp_wait(full0 + ring.slot * 8, ring.parity, abort_flag)) {
+            if (!issue_wait(full0 + ring.slot * 8, ring.parity, abort_flag)) {
               stop = true;
               break;
             }
@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int nb0 = x.n0 + static_cast<int>(rank) * 128;
       int k0 = x.k0;
       for (int l = 0; l < x.kb; ++l) {
-        if (!warp_wait(empty0 + ring.slot * 8, ring.parity ^ 1u, abort_flag)) {
+        if (!issue_wait(empty0 + ring.slot * 8, ring.parity ^ 1u, abort_flag)) {
           stop = true;
           break;
         }
@@ -691,7 +691,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         RingPos<STAGES> tail = ring;  // where the partial stage is
         for (int kb = 0; kb < x.kb; ++kb) {
           const int c = kb % CHUNK_KB;
-          if (c == 0 && !warp_wait(acce0 + au.slot * 8, au.parity ^ 1u, abort_flag)) {
+          if (c == 0 && !issue_wait(acce0 + au.slot * 8, au.parity ^ 1u, abort_flag)) {
             stop = true;
             break;
           }
@@ -702,7 +702,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           const bool last = kb == x.kb - 1, partial = last && x.tail != 0;
           const RingPos<STAGES> at = partial ? tail : ring;
-          if (!warp_wait(full0 + at.slot * 8, at.parity, abort_flag)) {
+          if (!issue_wait(full0 + at.slot * 8, at.parity, abort_flag)) {
             stop = true;
             break;
           }

@@ -326,16 +326,20 @@ __global__ void __launch_bounds__(256)
 //
 // C[b] = A[b] B[b]^T (A: M x K, B: N x K, both quantised along K).
 // k_mx4_gemm is a persistent CTA-pair kernel: one block-scaled tcgen05.mma
-// (kind::mxf4, K = 64, M = 256 over two SMs, N = 256) per 64 columns of K;
-// the tensor core multiplies each block's sum by both scales.  A stage is 256
-// columns: 128-byte rows of codes (128 of A and 128 of B per CTA) and the
-// scale tiles of this CTA's 128 rows of A and of all 256 rows of B, which
+// (kind::mxf4, K = 64, M = 256 over two SMs, N = NB = 256 or 128) per 64 columns
+// of K; the tensor core multiplies each block's sum by both scales.  A stage is
+// 256 columns: 128-byte rows of codes (128 of A and NB / 2 of B per CTA) and the
+// scale tiles of this CTA's 128 rows of A and of all NB rows of B, which
 // tcgen05.cp moves into tensor memory in front of the stage's MMAs.
 //
-// Tensor memory (512 columns): two 256-column accumulators at 0 and 192 and
-// two stages of scales behind them at 448.  The accumulators share 64 columns:
-// the epilogue drains those first and hands them back, so the next tile's
-// MMAs run beside the rest of this tile's epilogue.
+// Tensor memory (512 columns): two accumulators at 0 and 192 and two stages of
+// scales behind them at 448.  Accumulators of 256 columns share 64: the epilogue
+// drains those first and hands them back, so the next tile's MMAs run beside the
+// rest of this tile's epilogue.
+//
+// The issuing warp needs ten or so instructions per stage beside its waits, so
+// where a stage's MMAs are short it sets the rate: it asks whether the next stage
+// is full while it still issues this one (NB = 128: 203 -> 173 ns per stage).
 //
 // fp32 results are summed in chunks of CHUNK_KB stages (32 MMAs) in the tensor
 // core, which adds with truncation, and over chunks in registers.
@@ -344,22 +348,27 @@ __global__ void __launch_bounds__(256)
 // bytes per clock, about what the path from L2 delivers: 8192 x 8192 x 4096 97 us
 // = 5.67 PFLOP/s in a short run, 589 clocks per stage; under the power cap 119 us.
 
-constexpr int BN = 256;
-constexpr int MK = 256;            // codes per stage row: 128 bytes
-constexpr int TILE_BYTES = 128 * 128;
-constexpr int SF_BYTES = 3 * 1024;  // 2 tiles of A's rows, 2 x 2 of B's
-constexpr int STAGE_BYTES = 2 * TILE_BYTES + SF_BYTES;
-constexpr int STAGES = 5;
+constexpr int MK = 256;  // codes per stage row: 128 bytes
 constexpr int CHUNK_KB = 8;
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 32 * (2 + EPI_WARPS);
 constexpr int EPI_BOX = 4096;
-constexpr int GSMEM = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * EPI_BOX + 256;
 constexpr int ACC1 = 192;    // second accumulator's first column
 constexpr int SF_COL = 448;  // scales: per stage 8 columns of A, 16 of B
-static_assert(STAGE_BYTES % 1024 == 0, "swizzled tiles start on 1024-byte boundaries");
-static_assert(GSMEM <= 232448, "product kernel exceeds shared memory");
-static_assert(ACC1 + BN == SF_COL && SF_COL + 2 * 24 <= 512, "tensor memory");
+static_assert(ACC1 + 256 == SF_COL && SF_COL + 2 * 24 <= 512, "tensor memory");
+
+// NB columns of C per tile.
+template <int NB>
+struct GCfg {
+  static constexpr int A_BYTES = 128 * 128;
+  static constexpr int B_BYTES = NB / 2 * 128;
+  static constexpr int SB = NB > 128 ? 2 : 1;  // 128-row scale tiles of B
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + (1 + SB) * 1024;
+  static constexpr int STAGES = NB == 256 ? 5 : 7;
+  static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * EPI_BOX + 256;
+  static_assert(STAGE_BYTES % 1024 == 0, "swizzled tiles start on 1024-byte boundaries");
+  static_assert(SMEM <= 232448, "product kernel exceeds shared memory");
+};
 
 // One scale tile (32 rows of 16 bytes) to four columns of tensor memory,
 // repeated in all four lane quarters, in both CTAs of the pair (each from its
@@ -399,12 +408,14 @@ struct Mx4Params {
   int* status;     // bounded-wait self-test: receives SHP_ETIMEOUT (else null)
 };
 
-template <bool F32>
+template <int NB, bool F32>
 __global__ void __launch_bounds__(THREADS, 1)
     k_mx4_gemm(const __grid_constant__ CUtensorMap tA, const __grid_constant__ CUtensorMap tAs,
                const __grid_constant__ CUtensorMap tB, const __grid_constant__ CUtensorMap tBs,
                const __grid_constant__ CUtensorMap tO, Mx4Params p) {
   count_kernel_run();
+  using C = GCfg<NB>;
+  constexpr int STAGES = C::STAGES, STAGE_BYTES = C::STAGE_BYTES;
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
   const int ncl = static_cast<int>(gridDim.x) / 2, cl = static_cast<int>(blockIdx.x) / 2;
@@ -462,19 +473,19 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int b = t / per_b, r = t % per_b;
       const int tm = r / p.tiles_n, tn = r % p.tiles_n;
       const int m0 = tm * 256 + static_cast<int>(rank) * 128;
-      const int nb0 = tn * BN + static_cast<int>(rank) * 128;
+      const int nb0 = tn * NB + static_cast<int>(rank) * (NB / 2);
       const int za = b * p.rb_a + tm * 2 + static_cast<int>(rank);
-      const int zb = b * p.rb_b + tn * 2;
+      const int zb = b * p.rb_b + tn * NB / 128;
       for (int kb = 0; kb < KB; ++kb) {
-        if (!warp_wait(empty0 + ring.slot * 8, ring.parity ^ 1u, abort_flag)) {
+        if (!issue_wait(empty0 + ring.slot * 8, ring.parity ^ 1u, abort_flag)) {
           stop = true;
           break;
         }
-        const uint32_t sa = stages + ring.slot * STAGE_BYTES, sf = sa + 2 * TILE_BYTES;
+        const uint32_t sa = stages + ring.slot * STAGE_BYTES, sf = sa + C::A_BYTES + C::B_BYTES;
         const uint32_t fbar = fleader + ring.slot * 8;
         mbar_expect_tx_if(lead, full0 + ring.slot * 8, 2 * STAGE_BYTES);
         tma_3d_pair_if(on, sa, &tA, fbar, kb * 64, m0, b);  // codes move as 16-bit units
-        tma_3d_pair_if(on, sa + TILE_BYTES, &tB, fbar, kb * 64, nb0, b);
+        tma_3d_pair_if(on, sa + C::A_BYTES, &tB, fbar, kb * 64, nb0, b);
         tma_3d_pair_if(on, sf, &tAs, fbar, 0, kb * 2, za);
         tma_4d_pair_if(on, sf + 1024, &tBs, fbar, 0, kb * 2, zb, 0);
         ring.advance();
@@ -496,22 +507,22 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
       const uint32_t accf0 = smem_u32(accf), acce0 = smem_u32(acce);
       const uint64_t adesc = smem_desc(smem_u32(smem), 16, 1024u, 2u);
-      const uint64_t bdesc = smem_desc(smem_u32(smem) + TILE_BYTES, 16, 1024u, 2u);
-      const uint64_t sdesc = smem_desc(smem_u32(smem) + 2 * TILE_BYTES, 128, 128, 0);
+      const uint64_t bdesc = smem_desc(smem_u32(smem) + C::A_BYTES, 16, 1024u, 2u);
+      const uint64_t sdesc = smem_desc(smem_u32(smem) + C::A_BYTES + C::B_BYTES, 128, 128, 0);
       uint32_t u = 0, pe = 1;  // accumulator; parity of acce's last use
       uint32_t sf = 0;         // scale buffer
-      bool stop = gave_up;
+      bool stop = gave_up, ready = false;
       for (int t = cl; t < ntiles && !stop; t += ncl) {
         for (int c0 = 0; c0 < KB && !stop; c0 += F32 ? CHUNK_KB : KB, u ^= 1u, pe ^= 1u) {
           const int c1 = F32 ? min(c0 + CHUNK_KB, KB) : KB;
-          if (!warp_wait(acce0, pe, abort_flag)) {
+          if (!issue_wait(acce0, pe, abort_flag)) {
             stop = true;
             break;
           }
           tc_fence_after();
           const uint32_t dacc = tmem + u * ACC1;
           for (int kb = c0; kb < c1; ++kb) {
-            if (!warp_wait(full0 + ring.slot * 8, ring.parity, abort_flag)) {
+            if (!ready && !issue_wait(full0 + ring.slot * 8, ring.parity, abort_flag)) {
               stop = true;
               break;
             }
@@ -525,17 +536,19 @@ __global__ void __launch_bounds__(THREADS, 1)
               if (k * 128 >= left) break;
               tmem_cp_scales_pair_if(on, tsa + k * 4, sdesc + at + k * 32);
               tmem_cp_scales_pair_if(on, tsb + k * 8, sdesc + at + 64 + k * 32);
-              tmem_cp_scales_pair_if(on, tsb + k * 8 + 4, sdesc + at + 128 + k * 32);
+              if (C::SB == 2) tmem_cp_scales_pair_if(on, tsb + k * 8 + 4, sdesc + at + 128 + k * 32);
             }
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
               if (ks * 64 >= left) break;
               mma_mxf4_pair_if(on, dacc, adesc + at + ks * 2, bdesc + at + ks * 2,
-                               instr_desc_mxf4(256, BN, (ks & 1) * 2), tsa + (ks >> 1) * 4,
+                               instr_desc_mxf4(256, NB, (ks & 1) * 2), tsa + (ks >> 1) * 4,
                                tsb + (ks >> 1) * 8, (kb > c0 || ks > 0) ? 1u : 0u);
             }
-            mma_commit_pair_if(on, empty0 + ring.slot * 8, 3);
+            const uint32_t ebar = empty0 + ring.slot * 8;
             ring.advance();
+            ready = warp_test(full0 + ring.slot * 8, ring.parity);
+            mma_commit_pair_if(on, ebar, 3);
           }
           mma_commit_pair_if(on, accf0 + u * 8, 3);
         }
@@ -552,15 +565,19 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int t = cl; t < ntiles && !stop; t += ncl) {
       const int b = t / per_b, r = t % per_b;
       const int row0 = r / p.tiles_n * 256 + static_cast<int>(rank) * 128 + q * 32;
-      // warp half h owns columns 128h .. 128h + 127 and reads its two 64-column
-      // parts in the order that drains the shared columns first: they are the
-      // upper part of half 1 in accumulator 0, the lower part of half 0 in 1
-      const int n0 = r % p.tiles_n * BN + h * 128;
+      // warp half h owns half of the tile's columns; where they are 128 it reads
+      // its two 64-column parts in the order that drains the shared columns first:
+      // they are the upper part of half 1 in accumulator 0, the lower part of half
+      // 0 in 1
+      const int c0 = h * (NB / 2);
+      const int n0 = r % p.tiles_n * NB + c0;
       if (F32) {
-        float acc[128];
+        constexpr int PARTS = NB / 64;
+        const int flip = NB == 256 ? 2 * h : 0;
+        float acc[NB / 2];
 #pragma unroll
-        for (int j = 0; j < 128; ++j) acc[j] = 0.f;
-        for (int c0 = 0; c0 < KB; c0 += CHUNK_KB, ++it) {
+        for (int j = 0; j < NB / 2; ++j) acc[j] = 0.f;
+        for (int kc = 0; kc < KB; kc += CHUNK_KB, ++it) {
           const int u = it & 1;
           if (!warp_wait(smem_u32(&accf[u]), (it >> 1) & 1, abort_flag)) {
             stop = true;
@@ -568,9 +585,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           tc_fence_after();
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
+          for (int g = 0; g < PARTS; ++g) {
             float v[32];
-            tmem_ld32(trow + static_cast<uint32_t>(u * ACC1 + h * 128 + (g ^ (2 * h)) * 32), v);
+            tmem_ld32(trow + static_cast<uint32_t>(u * ACC1 + c0 + (g ^ flip) * 32), v);
 #pragma unroll
             for (int j = 0; j < 32; ++j) acc[g * 32 + j] += v[j];
             if (g == 1) {
@@ -583,8 +600,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (stop) break;
         if (row0 < p.M) {
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const int cb = n0 + (g ^ (2 * h)) * 32;
+          for (int g = 0; g < PARTS; ++g) {
+            const int cb = n0 + (g ^ flip) * 32;
             if (cb >= p.N) continue;
             if (lane == 0) bulk_wait_read_all();  // the previous store has read the box
             __syncwarp();
@@ -607,10 +624,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         ++it;
         tc_fence_after();
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const int part = (g ^ h) * 64;
+        for (int g = 0; g < (NB == 256 ? 2 : 1); ++g) {
+          const int part = NB == 256 ? (g ^ h) * 64 : 0;
           uint32_t w[64];
-          tmem_ld64_async(trow + static_cast<uint32_t>(u * ACC1 + h * 128 + part), w);
+          tmem_ld64_async(trow + static_cast<uint32_t>(u * ACC1 + c0 + part), w);
           tmem_ld_wait();
           if (g == 0) {
             tc_fence_before();
@@ -711,6 +728,52 @@ cudaError_t mx4_dequantize(const uint8_t* Q, const uint8_t* S, int rows, int col
   return cudaGetLastError();
 }
 
+namespace {
+
+template <int NB, bool F32>
+cudaError_t launch_gemm(const uint8_t* A, const uint8_t* As, const uint8_t* B, const uint8_t* Bs,
+                        void* O, Mx4Params p, cudaStream_t st) {
+  using C = GCfg<NB>;
+  p.tiles_m = static_cast<int>(ceil_div(p.M, 256));
+  p.tiles_n = static_cast<int>(ceil_div(p.N, NB));
+  const int64_t kt = ceil_div(p.K, 128);
+  const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.batch;
+  if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
+  CUtensorMap a, as, b, bs, o;
+  const int64_t u = p.K / 4;  // 16-bit units per row of codes
+  if (!tensor_map(&a, A, 2, u, p.M, p.batch, u, u * p.M, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !tensor_map(&b, B, 2, u, p.N, p.batch, u, u * p.N, 64, NB / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !tensor_map(&as, As, 4, 128, kt, p.batch * p.rb_a, 128, 128 * kt, 128, 2,
+                  CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !tensor_map4(&bs, Bs, 4, {128, kt, p.batch * p.rb_b, 1},
+                   {128, 128 * kt, 128 * kt * p.batch * p.rb_b}, {128, 2, C::SB, 1},
+                   CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !tensor_map(&o, O, F32 ? 4 : 2, p.N, p.M, p.batch, p.N, static_cast<int64_t>(p.M) * p.N,
+                  F32 ? 32 : 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  auto kern = k_mx4_gemm<NB, F32>;
+  static std::atomic<uint64_t> done{0};
+  const LaunchInfo li = launch_info(reinterpret_cast<const void*>(kern), C::SMEM, done);
+  if (li.err != cudaSuccess) return li.err;
+  int64_t ncl = li.sms / 2;
+  if (ncl > tiles) ncl = tiles;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * ncl), 1, 1);
+  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a, as, b, bs, o, p);
+}
+
+}  // namespace
+
 cudaError_t mx4_gemm(const uint8_t* A, const uint8_t* As, const uint8_t* B, const uint8_t* Bs,
                      void* C, bool f32, int M, int N, int K, int64_t batch, cudaStream_t st,
                      int* selftest) {
@@ -721,45 +784,21 @@ cudaError_t mx4_gemm(const uint8_t* A, const uint8_t* As, const uint8_t* B, cons
   p.N = N;
   p.K = K;
   p.batch = batch;
-  p.tiles_m = static_cast<int>(ceil_div(M, 256));
-  p.tiles_n = static_cast<int>(ceil_div(N, BN));
   p.rb_a = static_cast<int>(ceil_div(M, 128));
   p.rb_b = static_cast<int>(ceil_div(N, 128));
-  const int64_t kt = ceil_div(K, 128);
-  const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n * batch;
-  if (tiles > INT32_MAX / 2 || batch * p.rb_a > INT32_MAX || batch * p.rb_b > INT32_MAX)
-    return cudaErrorInvalidValue;
-  CUtensorMap a, as, b, bs, o;
-  const int64_t u = K / 4;  // 16-bit units per row of codes
-  if (!tensor_map(&a, A, 2, u, M, batch, u, u * M, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !tensor_map(&b, B, 2, u, N, batch, u, u * N, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !tensor_map(&as, As, 4, 128, kt, batch * p.rb_a, 128, 128 * kt, 128, 2,
-                  CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      !tensor_map4(&bs, Bs, 4, {128, kt, batch * p.rb_b, 1},
-                   {128, 128 * kt, 128 * kt * batch * p.rb_b}, {128, 2, 2, 1},
-                   CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      !tensor_map(&o, C, f32 ? 4 : 2, N, M, batch, N, static_cast<int64_t>(M) * N, f32 ? 32 : 64, 32,
-                  CU_TENSOR_MAP_SWIZZLE_128B))
-    return cudaErrorInvalidValue;
-  auto kern = f32 ? k_mx4_gemm<true> : k_mx4_gemm<false>;
-  static std::atomic<uint64_t> done[2];
-  const LaunchInfo li = launch_info(reinterpret_cast<const void*>(kern), GSMEM, done[f32 ? 1 : 0]);
-  if (li.err != cudaSuccess) return li.err;
-  int64_t ncl = li.sms / 2;
-  if (ncl > tiles) ncl = tiles;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * ncl), 1, 1);
-  cfg.blockDim = dim3(THREADS, 1, 1);
-  cfg.dynamicSmemBytes = GSMEM;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, a, as, b, bs, o, p);
+  if (batch * p.rb_a > INT32_MAX || batch * p.rb_b > INT32_MAX) return cudaErrorInvalidValue;
+  // Tiles of 128 columns where those of 256 leave half of the SM pairs idle: a
+  // stage of a tile then takes 173 ns, not 290 (16 x 4096 x 4096 8.4 us, not 9.5;
+  // 256 x 8192 x 8192 12.4 us, not 15.7; 36 blocks of 100 x 200 x 512 5.9 us, not
+  // 6.5; fp32 results gain more).  With more tiles they need more rounds (40
+  // tiles, 1376 columns: 8.8 against 8.9 us; 112 tiles, 4096: 20.1 against 17.3).
+  const int64_t pairs = 74;
+  const int64_t wide = ceil_div(M, 256) * ceil_div(N, 256) * batch;
+  if (2 * wide <= pairs)
+    return f32 ? launch_gemm<128, true>(A, As, B, Bs, C, p, st)
+               : launch_gemm<128, false>(A, As, B, Bs, C, p, st);
+  return f32 ? launch_gemm<256, true>(A, As, B, Bs, C, p, st)
+             : launch_gemm<256, false>(A, As, B, Bs, C, p, st);
 }
 
 uint64_t kernel_runs_mx4() {

@@ -192,6 +192,46 @@ def test_product_picks_every_scale():
         np.testing.assert_array_equal(C.cpu().numpy(), a.astype(np.float64) @ b.astype(np.float64).transpose(0, 2, 1))
 
 
+# many tiles: these run in tiles of 256 columns, the few of the sizes above in tiles of 128
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("batch,M,N,K", [(5, 700, 1032, 1376), (40, 130, 264, 288), (38, 1, 8, 32), (1, 2500, 1800, 4192),
+                                         (37, 256, 256, 96), (38, 256, 256, 96), (2, 100, 5000, 2080)])
+def test_product_many_tiles(batch, M, N, K, dtype):
+    A, As, a = operand(batch, M, K, 13)
+    B, Bs, b = operand(batch, N, K, 14)
+    C = P().shp_mx4_matmul(A, As, B, Bs, dtype=dtype)
+    check_product(C, a, b)
+
+
+def test_product_same_in_both_tile_widths():
+    """A block alone (few tiles) and in a batch (many): the same bits."""
+    A, As, _ = operand(40, 300, 1376, 15)
+    B, Bs, _ = operand(40, 520, 1376, 16)
+    for dtype in (torch.float32, torch.bfloat16):
+        C = P().shp_mx4_matmul(A, As, B, Bs, dtype=dtype)
+        for i in (0, 17, 39):
+            one = P().shp_mx4_matmul(A[i:i + 1], As[i:i + 1], B[i:i + 1], Bs[i:i + 1], dtype=dtype)
+            assert torch.equal(one[0], C[i])
+
+
+def test_product_picks_every_scale_of_many_tiles():
+    """test_product_picks_every_scale where tiles have 256 columns."""
+    M, N, K = 2304, 1544, 288
+    rows, blocks = torch.arange(M)[:, None], torch.arange(K // 32)[None, :]
+    exps = ((rows * 7 + blocks * 5) % 23 - 11).double()
+    for k in range(K // 32):
+        a = torch.zeros(1, M, K, dtype=torch.float64)
+        a[0, :, k * 32] = torch.exp2(exps[:, k])
+        b = torch.zeros(1, N, K, dtype=torch.float64)
+        b[0, :, k * 32] = torch.exp2(exps[:N, (k + 3) % (K // 32)])
+        a, b = a.cuda(), b.cuda()
+        A, As = P().shp_mx4_quantize(a.float())
+        B, Bs = P().shp_mx4_quantize(b.float())
+        C = P().shp_mx4_matmul(A, As, B, Bs, dtype=torch.float32)
+        ref = a[0, :, k * 32, None] * b[0, None, :, k * 32]
+        assert torch.equal(C[0].double(), ref)
+
+
 def test_nan_block_reaches_its_row_alone():
     X = rand((1, 300, 256), 5, torch.float32)
     X[0, 77, 40] = float("nan")
