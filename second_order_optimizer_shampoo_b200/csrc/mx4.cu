@@ -344,9 +344,10 @@ __global__ void __launch_bounds__(256)
 // fp32 results are summed in chunks of CHUNK_KB stages (32 MMAs) in the tensor
 // core, which adds with truncation, and over chunks in registers.
 //
-// Bound and rate: a stage brings 35 KB into each SM for 512 clocks of MMAs, 68
-// bytes per clock, about what the path from L2 delivers: 8192 x 8192 x 4096 97 us
-// = 5.67 PFLOP/s in a short run, 589 clocks per stage; under the power cap 119 us.
+// Bound and rate: a stage of NB = 256 brings 35 KB into each SM for 512 clocks of
+// MMAs, 68 bytes per clock, about what the path from L2 delivers: 8192 x 8192 x
+// 4096 93 us = 5.9 PFLOP/s in a short run, about 550 clocks per stage; under the
+// power cap 116 us.
 
 constexpr int MK = 256;  // codes per stage row: 128 bytes
 constexpr int CHUNK_KB = 8;
