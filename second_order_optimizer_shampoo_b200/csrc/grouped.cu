@@ -455,8 +455,9 @@ __global__ void __launch_bounds__(RowsCfg<NT, F32>::THREADS, 1)
 // thousand rows the busiest pair has 1 % more stages than the mean, in a fixed
 // rotation 10 %.
 // Bound and rate: tensor pipe for long groups (that case, 1024 x 4096,
-// accumulated: 422 us = 1303 TFLOP/s in a short run), the stores of G for short
-// ones (64 groups of 256 rows, 1024^2: 64 us for 335 MB = 5.2 TB/s).
+// accumulated: 414 us = 1328 TFLOP/s in a short run), the stores of G for short
+// ones (64 groups of 256 rows, 1024^2: 61 us for 335 MB = 5.5 TB/s; a kernel that
+// only stores such tiles takes 50 us for their 268 MB).
 
 constexpr int STAGE_BYTES = 2 * A_BYTES;
 constexpr int STAGES = 6;
