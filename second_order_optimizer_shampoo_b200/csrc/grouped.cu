@@ -24,7 +24,14 @@
 //     about half an ulp per MMA that grows with the length of the sum, so
 //     fp32 results are summed in chunks of CHUNK_KB stages: each chunk is
 //     read out of TMEM and added to running sums in registers, rounded to
-//     nearest, while the next chunk's MMAs run.  bf16 results take one chunk.
+//     nearest, while the next chunk's MMAs run.  bf16 results take chunks of
+//     LONG_KB stages: 256 MMAs' bias, at most 2^-16 of a sum of one sign, moves
+//     one bf16 result in 500 to its neighbour, and a longer contraction's is no
+//     larger.  Up to that length a chunk is the whole sum and is stored as it
+//     leaves the accumulator (chunks of CHUNK_KB for bf16 too: 65536 rows over
+//     16 groups, 4096 x 1024, 405 us against 372, and 1024 x 4096 466 against
+//     381; the error against the exact product is its rounding's, 1.7e-3 of the
+//     norm, either way).
 #include <cuda_bf16.h>
 #include <string.h>
 
@@ -38,6 +45,7 @@ namespace {
 constexpr int BK = 64;                // contraction elements per stage: 128-byte rows
 constexpr int A_BYTES = 128 * 128;    // per CTA and stage: 128 rows (columns) of A
 constexpr int CHUNK_KB = 8;  // stages per fp32 chunk: sums of 512 products inside the tensor core
+constexpr int LONG_KB = 64;  // stages per chunk of a bf16 result: sums of 4096 products
 constexpr int EPI_WARPS = 8;
 constexpr int EPI_BOX = 4096;  // one warp's 32 x 32 fp32 store box
 
@@ -166,6 +174,9 @@ struct RowsParams {
   int* status;   // bounded-wait self-test: receives SHP_ETIMEOUT (else null)
 };
 
+// What a tile's sums become: bf16 of one accumulator, bf16 or fp32 of summed chunks.
+enum RowsOut { OUT_BF16, OUT_BF16_CHUNKS, OUT_F32 };
+
 template <int NT, bool F32>
 struct RowsCfg {
   static constexpr int X_BYTES = NT / 2 * 128;
@@ -177,12 +188,14 @@ struct RowsCfg {
   static constexpr int THREADS = 32 * (2 + EPI_WARPS + 1);
 };
 
-template <int NT, bool W_MN, bool F32>
-__global__ void __launch_bounds__(RowsCfg<NT, F32>::THREADS, 1)
+template <int NT, bool W_MN, RowsOut OUT>
+__global__ void __launch_bounds__(RowsCfg<NT, OUT == OUT_F32>::THREADS, 1)
     k_grouped_rows(const __grid_constant__ CUtensorMap tW, const __grid_constant__ CUtensorMap tX,
                    const __grid_constant__ CUtensorMap tX32,
                    const __grid_constant__ CUtensorMap tY, RowsParams p) {
   count_kernel_run();
+  constexpr bool F32 = OUT == OUT_F32, CHUNKS = OUT != OUT_BF16;
+  constexpr int CHUNK = F32 ? CHUNK_KB : LONG_KB;
   using C = RowsCfg<NT, F32>;
   constexpr int STAGES = C::STAGES;
   const uint32_t rank = cluster_rank();
@@ -300,8 +313,8 @@ __global__ void __launch_bounds__(RowsCfg<NT, F32>::THREADS, 1)
       bool stop = gave_up;
       while (!stop && walk.next(x)) {
         const uint32_t idesc = instr_desc(1u, W_MN, false, 256, (x.count + 15) & ~15);
-        for (int c0 = 0; c0 < KB && !stop; c0 += F32 ? CHUNK_KB : KB, au.advance()) {
-          const int c1 = F32 ? min(c0 + CHUNK_KB, KB) : KB;
+        for (int c0 = 0; c0 < KB && !stop; c0 += CHUNKS ? CHUNK : KB, au.advance()) {
+          const int c1 = CHUNKS ? min(c0 + CHUNK, KB) : KB;
           if (!issue_wait(acce0 + au.slot * 8, au.parity ^ 1u, abort_flag)) {
             stop = true;
             break;
@@ -352,11 +365,26 @@ __global__ void __launch_bounds__(RowsCfg<NT, F32>::THREADS, 1)
     bool stop = false;
     while (!stop && walk.next(x)) {
       const int nb = x.n0 + static_cast<int>(rank) * 128 + q * 32;  // this warp's first column
-      if (F32) {
+      // bf16: lane l stores columns nb + (l & ~1), + 1 of the even (odd) rows from r0 on
+      const int odd = lane & 1;
+      const bool in = nb + lane < p.N;  // N is even: a pair is in or out
+      auto store_bf16 = [&](int r0, const float* v) {
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) +
+                           static_cast<int64_t>(x.t0 + r0 + odd) * p.N + nb + lane - odd;
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+          const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+          const __nv_bfloat162 w = odd ? __floats2bfloat162_rn(got, v[j + 1])
+                                       : __floats2bfloat162_rn(v[j], got);
+          if (in && r0 + j + odd < x.count)
+            *reinterpret_cast<__nv_bfloat162*>(o + static_cast<int64_t>(j) * p.N) = w;
+        }
+      };
+      if (CHUNKS) {
         float acc[NC * 32];
 #pragma unroll
         for (int j = 0; j < NC * 32; ++j) acc[j] = 0.f;
-        for (int c0 = 0; c0 < KB; c0 += CHUNK_KB, ++it) {
+        for (int c0 = 0; c0 < KB; c0 += CHUNK, ++it) {
           const int u = it & 1;
           if (!warp_wait(smem_u32(&accf[u]), (it >> 1) & 1, abort_flag)) {
             stop = true;
@@ -377,7 +405,11 @@ __global__ void __launch_bounds__(RowsCfg<NT, F32>::THREADS, 1)
           if (lane == 0) mbar_arrive_relaxed(mapa_shared(smem_u32(&acce[u]), 0));
         }
         if (stop) break;
-        if (nb < p.N) {
+        if (!F32) {
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+            if ((2 * c + h) * 32 < x.count) store_bf16((2 * c + h) * 32, acc + c * 32);
+        } else if (nb < p.N) {
           uint8_t* box = boxes + (warp - 2) * EPI_BOX;
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
@@ -408,23 +440,11 @@ __global__ void __launch_bounds__(RowsCfg<NT, F32>::THREADS, 1)
         if (!warp_wait(smem_u32(&accf[u]), (it >> 1) & 1, abort_flag)) break;
         ++it;
         tc_fence_after();
-        // lane l stores columns nb + (l & ~1), + 1 of the even (odd) rows
-        const int odd = lane & 1;
-        const bool in = nb + lane < p.N;  // N is even: a pair is in or out
 #pragma unroll 1
         for (int r0 = h * 32; r0 < x.count; r0 += 64) {
           float v[32];
           tmem_ld32(trow + static_cast<uint32_t>(u * NT + r0), v);
-          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) +
-                             static_cast<int64_t>(x.t0 + r0 + odd) * p.N + nb + lane - odd;
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
-            const __nv_bfloat162 w = odd ? __floats2bfloat162_rn(got, v[j + 1])
-                                         : __floats2bfloat162_rn(v[j], got);
-            if (in && r0 + j + odd < x.count)
-              *reinterpret_cast<__nv_bfloat162*>(o + static_cast<int64_t>(j) * p.N) = w;
-          }
+          store_bf16(r0, v);
         }
         tc_fence_before();
         __syncwarp();
@@ -866,11 +886,11 @@ cudaLaunchConfig_t pair_grid(int64_t pairs, int threads, int smem, cudaStream_t 
   return cfg;
 }
 
-template <int NT, bool W_MN, bool F32>
+template <int NT, bool W_MN, RowsOut OUT>
 cudaError_t launch_rows(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& x32,
                         const CUtensorMap& y, RowsParams p, int T, cudaStream_t st) {
-  using C = RowsCfg<NT, F32>;
-  auto kern = k_grouped_rows<NT, W_MN, F32>;
+  using C = RowsCfg<NT, OUT == OUT_F32>;
+  auto kern = k_grouped_rows<NT, W_MN, OUT>;
   static std::atomic<uint64_t> done{0};
   const LaunchInfo li = launch_info(reinterpret_cast<const void*>(kern), C::SMEM, done);
   if (li.err != cudaSuccess) return li.err;
@@ -890,6 +910,15 @@ cudaError_t launch_rows(const CUtensorMap& w, const CUtensorMap& x, const CUtens
   return cudaLaunchKernelEx(&cfg, kern, w, x, x32, y, p);
 }
 
+template <int NT, bool W_MN>
+cudaError_t dispatch_out(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& x32,
+                         const CUtensorMap& y, bool f32, const RowsParams& p, int T,
+                         cudaStream_t st) {
+  if (f32) return launch_rows<NT, W_MN, OUT_F32>(w, x, x32, y, p, T, st);
+  return p.K > LONG_KB * BK ? launch_rows<NT, W_MN, OUT_BF16_CHUNKS>(w, x, x32, y, p, T, st)
+                      : launch_rows<NT, W_MN, OUT_BF16>(w, x, x32, y, p, T, st);
+}
+
 template <int NT>
 cudaError_t dispatch_rows(const void* X, const CUtensorMap& w, bool w_mn, bool f32,
                           const RowsParams& p, int T, cudaStream_t st) {
@@ -900,11 +929,8 @@ cudaError_t dispatch_rows(const void* X, const CUtensorMap& w, bool w_mn, bool f
   if (!tensor_map(&x, X, 2, p.K, T, 1, p.K, 0, BK, NT / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !tensor_map(&x32, X, 2, p.K, T, 1, p.K, 0, BK, 32, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  if (w_mn)
-    return f32 ? launch_rows<NT, true, true>(w, x, x32, y, p, T, st)
-               : launch_rows<NT, true, false>(w, x, x32, y, p, T, st);
-  return f32 ? launch_rows<NT, false, true>(w, x, x32, y, p, T, st)
-             : launch_rows<NT, false, false>(w, x, x32, y, p, T, st);
+  return w_mn ? dispatch_out<NT, true>(w, x, x32, y, f32, p, T, st)
+              : dispatch_out<NT, false>(w, x, x32, y, f32, p, T, st);
 }
 
 // Rows per tile.  The host knows the mean size of a group only, so it counts as

@@ -342,7 +342,10 @@ __global__ void __launch_bounds__(256)
 // is full while it still issues this one (NB = 128: 203 -> 173 ns per stage).
 //
 // fp32 results are summed in chunks of CHUNK_KB stages (32 MMAs) in the tensor
-// core, which adds with truncation, and over chunks in registers.
+// core, which adds with truncation, and over chunks in registers; bf16 results in
+// chunks of LONG_KB stages (256 MMAs: a bias of at most 2^-16 of a sum of one sign,
+// however long the contraction), which is the whole sum, stored as it leaves the
+// accumulator, where K is no longer.
 //
 // Bound and rate: a stage of NB = 256 brings 35 KB into each SM for 512 clocks of
 // MMAs, 68 bytes per clock, about what the path from L2 delivers: 8192 x 8192 x
@@ -350,7 +353,8 @@ __global__ void __launch_bounds__(256)
 // power cap 116 us.
 
 constexpr int MK = 256;  // codes per stage row: 128 bytes
-constexpr int CHUNK_KB = 8;
+constexpr int CHUNK_KB = 8;   // stages per chunk of an fp32 result
+constexpr int LONG_KB = 64;   // stages per chunk of a bf16 result
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 32 * (2 + EPI_WARPS);
 constexpr int EPI_BOX = 4096;
@@ -409,7 +413,10 @@ struct Mx4Params {
   int* status;     // bounded-wait self-test: receives SHP_ETIMEOUT (else null)
 };
 
-template <int NB, bool F32>
+// What a tile's sums become: bf16 of one accumulator, bf16 or fp32 of summed chunks.
+enum GemmOut { OUT_BF16, OUT_BF16_CHUNKS, OUT_F32 };
+
+template <int NB, GemmOut OUT>
 __global__ void __launch_bounds__(THREADS, 1)
     k_mx4_gemm(const __grid_constant__ CUtensorMap tA, const __grid_constant__ CUtensorMap tAs,
                const __grid_constant__ CUtensorMap tB, const __grid_constant__ CUtensorMap tBs,
@@ -417,6 +424,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   count_kernel_run();
   using C = GCfg<NB>;
   constexpr int STAGES = C::STAGES, STAGE_BYTES = C::STAGE_BYTES;
+  constexpr bool F32 = OUT == OUT_F32, CHUNKS = OUT != OUT_BF16;
+  constexpr int CHUNK = F32 ? CHUNK_KB : LONG_KB;
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
   const int ncl = static_cast<int>(gridDim.x) / 2, cl = static_cast<int>(blockIdx.x) / 2;
@@ -514,8 +523,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       uint32_t sf = 0;         // scale buffer
       bool stop = gave_up, ready = false;
       for (int t = cl; t < ntiles && !stop; t += ncl) {
-        for (int c0 = 0; c0 < KB && !stop; c0 += F32 ? CHUNK_KB : KB, u ^= 1u, pe ^= 1u) {
-          const int c1 = F32 ? min(c0 + CHUNK_KB, KB) : KB;
+        for (int c0 = 0; c0 < KB && !stop; c0 += CHUNKS ? CHUNK : KB, u ^= 1u, pe ^= 1u) {
+          const int c1 = CHUNKS ? min(c0 + CHUNK, KB) : KB;
           if (!issue_wait(acce0, pe, abort_flag)) {
             stop = true;
             break;
@@ -572,13 +581,33 @@ __global__ void __launch_bounds__(THREADS, 1)
       // 0 in 1
       const int c0 = h * (NB / 2);
       const int n0 = r % p.tiles_n * NB + c0;
-      if (F32) {
+      // a 32-row x 64-column part as bf16 pairs w[0..31], through the box
+      auto store_bf16 = [&](int part, const uint32_t* w) {
+        if (row0 >= p.M || n0 + part >= p.N) return;
+        if (lane == 0) bulk_wait_read_all();
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4*>(box + sw128_off(lane, i)) =
+              make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(&tO, box, n0 + part, row0, b);
+          bulk_commit();
+        }
+      };
+      auto pair_bf16 = [](float lo, float hi) {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&x);
+      };
+      if (CHUNKS) {
         constexpr int PARTS = NB / 64;
         const int flip = NB == 256 ? 2 * h : 0;
         float acc[NB / 2];
 #pragma unroll
         for (int j = 0; j < NB / 2; ++j) acc[j] = 0.f;
-        for (int kc = 0; kc < KB; kc += CHUNK_KB, ++it) {
+        for (int kc = 0; kc < KB; kc += CHUNK, ++it) {
           const int u = it & 1;
           if (!warp_wait(smem_u32(&accf[u]), (it >> 1) & 1, abort_flag)) {
             stop = true;
@@ -599,7 +628,16 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
         if (stop) break;
-        if (row0 < p.M) {
+        if (!F32) {
+#pragma unroll
+          for (int g = 0; g < PARTS; g += 2) {
+            uint32_t w[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              w[j] = pair_bf16(acc[g * 32 + 2 * j], acc[g * 32 + 2 * j + 1]);
+            store_bf16((g ^ flip) * 32, w);
+          }
+        } else if (row0 < p.M) {
 #pragma unroll
           for (int g = 0; g < PARTS; ++g) {
             const int cb = n0 + (g ^ flip) * 32;
@@ -636,25 +674,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (lane == 0) mbar_arrive_relaxed(mapa_shared(smem_u32(acce), 0));
           }
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const __nv_bfloat162 x =
-                __floats2bfloat162_rn(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
-            w[j] = *reinterpret_cast<const uint32_t*>(&x);
-          }
-          if (row0 < p.M && n0 + part < p.N) {
-            if (lane == 0) bulk_wait_read_all();
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<uint4*>(box + sw128_off(lane, i)) =
-                  make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_3d(&tO, box, n0 + part, row0, b);
-              bulk_commit();
-            }
-          }
+          for (int j = 0; j < 32; ++j)
+            w[j] = pair_bf16(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+          store_bf16(part, w);
         }
       }
     }
@@ -731,10 +753,11 @@ cudaError_t mx4_dequantize(const uint8_t* Q, const uint8_t* S, int rows, int col
 
 namespace {
 
-template <int NB, bool F32>
+template <int NB, GemmOut OUT>
 cudaError_t launch_gemm(const uint8_t* A, const uint8_t* As, const uint8_t* B, const uint8_t* Bs,
                         void* O, Mx4Params p, cudaStream_t st) {
   using C = GCfg<NB>;
+  constexpr bool F32 = OUT == OUT_F32;
   p.tiles_m = static_cast<int>(ceil_div(p.M, 256));
   p.tiles_n = static_cast<int>(ceil_div(p.N, NB));
   const int64_t kt = ceil_div(p.K, 128);
@@ -752,7 +775,7 @@ cudaError_t launch_gemm(const uint8_t* A, const uint8_t* As, const uint8_t* B, c
       !tensor_map(&o, O, F32 ? 4 : 2, p.N, p.M, p.batch, p.N, static_cast<int64_t>(p.M) * p.N,
                   F32 ? 32 : 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  auto kern = k_mx4_gemm<NB, F32>;
+  auto kern = k_mx4_gemm<NB, OUT>;
   static std::atomic<uint64_t> done{0};
   const LaunchInfo li = launch_info(reinterpret_cast<const void*>(kern), C::SMEM, done);
   if (li.err != cudaSuccess) return li.err;
@@ -771,6 +794,14 @@ cudaError_t launch_gemm(const uint8_t* A, const uint8_t* As, const uint8_t* B, c
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, a, as, b, bs, o, p);
+}
+
+template <int NB>
+cudaError_t dispatch_gemm(const uint8_t* A, const uint8_t* As, const uint8_t* B, const uint8_t* Bs,
+                          void* O, bool f32, const Mx4Params& p, cudaStream_t st) {
+  if (f32) return launch_gemm<NB, OUT_F32>(A, As, B, Bs, O, p, st);
+  return p.K > LONG_KB * MK ? launch_gemm<NB, OUT_BF16_CHUNKS>(A, As, B, Bs, O, p, st)
+                            : launch_gemm<NB, OUT_BF16>(A, As, B, Bs, O, p, st);
 }
 
 }  // namespace
@@ -795,11 +826,8 @@ cudaError_t mx4_gemm(const uint8_t* A, const uint8_t* As, const uint8_t* B, cons
   // tiles, 1376 columns: 8.8 against 8.9 us; 112 tiles, 4096: 20.1 against 17.3).
   const int64_t pairs = 74;
   const int64_t wide = ceil_div(M, 256) * ceil_div(N, 256) * batch;
-  if (2 * wide <= pairs)
-    return f32 ? launch_gemm<128, true>(A, As, B, Bs, C, p, st)
-               : launch_gemm<128, false>(A, As, B, Bs, C, p, st);
-  return f32 ? launch_gemm<256, true>(A, As, B, Bs, C, p, st)
-             : launch_gemm<256, false>(A, As, B, Bs, C, p, st);
+  return 2 * wide <= pairs ? dispatch_gemm<128>(A, As, B, Bs, C, f32, p, st)
+                           : dispatch_gemm<256>(A, As, B, Bs, C, f32, p, st);
 }
 
 uint64_t kernel_runs_mx4() {
