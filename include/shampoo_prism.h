@@ -328,7 +328,9 @@ int shp_split_tf32(const float* X, int64_t count, float* hi, float* lo, shp_stre
  *
  * These products and those of the 4-bit format below have no status to report:
  * a bounded wait inside their kernels that ran out (only a device fault can
- * cause that) leaves the result incomplete, as in shp_matmul. */
+ * cause that: a wait's limit is a second for a step of a pipeline, and grows
+ * with the tile where it spans one) leaves the result incomplete, as in
+ * shp_matmul. */
 
 /* Y[t] = X[t] W[e(t)] for every row t of every group: the forward product of
  * an expert layer, and with the other w_trans the gradient of its input.
@@ -454,6 +456,12 @@ int prism_alpha_fit_noalloc(const float* R, int64_t n, int64_t batch, const floa
  *                        in flight (they are waited for)
  *   SHP_SELFTEST_MX4_QUANTIZE  the 4-bit quantiser: the consumers' first wait,
  *                        with the producer's copies in flight
+ *   SHP_SELFTEST_GROUPED_LONG, SHP_SELFTEST_WGRAD_LONG,
+ *   SHP_SELFTEST_MX4_MATMUL_LONG  the other way round: launches of several long
+ *                        tiles, 2 to 25 times as long as the limit of a wait (set
+ *                        to 50 us), in which every step is far shorter.  No wait
+ *                        may run out: status stays 0.  ws_bytes at least
+ *                        SHP_SELFTEST_LONG_WS_BYTES
  * status: one device int32, set to SHP_ETIMEOUT by the kernel (cleared
  * first).  alpha_out: one device float (may be NULL), for the sketch cases
  * the fit's alpha, which must come out NaN (no fit on incomplete vectors; the
@@ -469,7 +477,11 @@ int prism_alpha_fit_noalloc(const float* R, int64_t n, int64_t batch, const floa
 #define SHP_SELFTEST_WGRAD 6
 #define SHP_SELFTEST_MX4_QUANTIZE 7
 #define SHP_SELFTEST_MX4_MATMUL 8
+#define SHP_SELFTEST_GROUPED_LONG 9
+#define SHP_SELFTEST_WGRAD_LONG 10
+#define SHP_SELFTEST_MX4_MATMUL_LONG 11
 #define SHP_SELFTEST_WS_BYTES (4u << 20)
+#define SHP_SELFTEST_LONG_WS_BYTES (128u << 20)
 int shp_selftest_bounded_wait(int which, int32_t* status, float* alpha_out, void* ws,
                               size_t ws_bytes, shp_stream stream);
 

@@ -29,7 +29,9 @@ SHP_SELFTEST_GEMM, SHP_SELFTEST_OZAKI, SHP_SELFTEST_SKETCH = 0, 1, 2
 SHP_SELFTEST_SKETCH_ALPHA, SHP_SELFTEST_SKETCH_CHAIN = 3, 4
 SHP_SELFTEST_GROUPED, SHP_SELFTEST_WGRAD = 5, 6
 SHP_SELFTEST_MX4_QUANTIZE, SHP_SELFTEST_MX4_MATMUL = 7, 8
+SHP_SELFTEST_GROUPED_LONG, SHP_SELFTEST_WGRAD_LONG, SHP_SELFTEST_MX4_MATMUL_LONG = 9, 10, 11
 SHP_SELFTEST_WS_BYTES = 4 << 20
+SHP_SELFTEST_LONG_WS_BYTES = 128 << 20
 # fixed device scratch of prism_alpha_fit_noalloc
 SHP_NOALLOC_SCRATCH_BYTES = 4 << 20
 

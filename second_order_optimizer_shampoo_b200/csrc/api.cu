@@ -975,16 +975,21 @@ extern "C" {
 
 int shp_selftest_bounded_wait(int which, int32_t* status, float* alpha_out, void* ws,
                               size_t ws_bytes, shp_stream stream) {
-  if (status == nullptr || ws == nullptr || ws_bytes < SHP_SELFTEST_WS_BYTES) return SHP_EINVAL;
-  if (which != SHP_SELFTEST_GEMM && which != SHP_SELFTEST_OZAKI && which != SHP_SELFTEST_SKETCH &&
+  const bool longer = which == SHP_SELFTEST_GROUPED_LONG || which == SHP_SELFTEST_WGRAD_LONG ||
+                      which == SHP_SELFTEST_MX4_MATMUL_LONG;
+  const size_t need = longer ? SHP_SELFTEST_LONG_WS_BYTES : SHP_SELFTEST_WS_BYTES;
+  if (status == nullptr || ws == nullptr || ws_bytes < need) return SHP_EINVAL;
+  if (!longer && which != SHP_SELFTEST_GEMM && which != SHP_SELFTEST_OZAKI && which != SHP_SELFTEST_SKETCH &&
       which != SHP_SELFTEST_SKETCH_ALPHA && which != SHP_SELFTEST_SKETCH_CHAIN &&
       which != SHP_SELFTEST_GROUPED && which != SHP_SELFTEST_WGRAD &&
       which != SHP_SELFTEST_MX4_QUANTIZE && which != SHP_SELFTEST_MX4_MATMUL)
     return SHP_EINVAL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   CK(cudaMemsetAsync(status, 0, sizeof(int32_t), st));
-  CK(cudaMemsetAsync(ws, 0, SHP_SELFTEST_WS_BYTES, st));
+  CK(cudaMemsetAsync(ws, 0, need, st));
   Arena a(reinterpret_cast<void*>((reinterpret_cast<uintptr_t>(ws) + kAlign - 1) & ~(kAlign - 1)));
+  // the long launches: 50 us per wait, where a step takes under 20
+  const SelfTest slow{status, 0, 100000};
   constexpr int n = 256, p = 8;  // one 256 x 256 product (a single CTA-pair tile)
   if (which == SHP_SELFTEST_GEMM) {
     float* A = a.take<float>(n * n);
@@ -1003,17 +1008,41 @@ int shp_selftest_bounded_wait(int which, int32_t* status, float* alpha_out, void
     float* C = a.take<float>(n * n);
     CK(cudaMemsetAsync(off + 1, 200, 1, st));  // offsets {0, 200}, little-endian
     if (which == SHP_SELFTEST_GROUPED)
-      CK(grouped_rows(A, off, B, false, C, 200, n, n, 1, true, st, status));
+      CK(grouped_rows(A, off, B, false, C, 200, n, n, 1, true, st, {status, 1}));
     else
-      CK(grouped_wgrad(A, B, off, C, 200, n, n, 1, false, st, status));
+      CK(grouped_wgrad(A, B, off, C, 200, n, n, 1, false, st, {status, 1}));
+  } else if (which == SHP_SELFTEST_GROUPED_LONG) {
+    // offsets 0, 4, 0, 4, ...: every second group is the same four rows, the others are
+    // empty; 20 tiles of 1024 stages for four CTA pairs
+    constexpr int E = 40, T = 4, K = 65536, N = 8;
+    int64_t* off = a.take<int64_t>(E + 1);
+    CK(cudaMemset2DAsync(off + 1, 16, T, 1, E / 2, st));
+    uint16_t* X = a.take<uint16_t>(static_cast<size_t>(T) * K);
+    uint16_t* W = a.take<uint16_t>(static_cast<size_t>(E) * K * N);
+    CK(grouped_rows(X, off, W, false, a.take<uint16_t>(T * N), T, K, N, E, false, st, slow));
+  } else if (which == SHP_SELFTEST_WGRAD_LONG) {
+    // the same with 65536 rows: 150 tiles of 1024 stages, handed out, and 150 empty ones
+    constexpr int E = 300, T = 65536, M = 8;
+    int64_t* off = a.take<int64_t>(E + 1);
+    CK(cudaMemset2DAsync(reinterpret_cast<uint8_t*>(off + 1) + 2, 16, T >> 16, 1, E / 2, st));
+    uint16_t* A = a.take<uint16_t>(static_cast<size_t>(T) * M);
+    CK(grouped_wgrad(A, A, off, a.take<float>(E * M * M), T, M, M, E, false, st, slow));
+  } else if (which == SHP_SELFTEST_MX4_MATMUL_LONG) {
+    // 400 tiles of 64 stages: no wait but the one for the end of the launch is long
+    constexpr int M = 5120, K = 16384;
+    uint8_t* Q = a.take<uint8_t>(shp_mx4_code_bytes(M, K, 1));
+    uint8_t* S = a.take<uint8_t>(shp_mx4_scale_bytes(M, K, 1));
+    CK(mx4_gemm(Q, S, Q, S, a.take<uint16_t>(static_cast<size_t>(M) * M), false, M, M, K, 1, st,
+                slow));
   } else if (which == SHP_SELFTEST_MX4_QUANTIZE) {
     uint8_t* Q = a.take<uint8_t>(shp_mx4_code_bytes(n, n, 1));
     uint8_t* S = a.take<uint8_t>(shp_mx4_scale_bytes(n, n, 1));
-    CK(mx4_quantize(a.take<float>(n * n), false, n, n, 1, Q, S, nullptr, nullptr, st, status));
+    CK(mx4_quantize(a.take<float>(n * n), false, n, n, 1, Q, S, nullptr, nullptr, st,
+                    {status, 1}));
   } else if (which == SHP_SELFTEST_MX4_MATMUL) {
     uint8_t* Q = a.take<uint8_t>(shp_mx4_code_bytes(n, 4 * n, 1));
     uint8_t* S = a.take<uint8_t>(shp_mx4_scale_bytes(n, 4 * n, 1));
-    CK(mx4_gemm(Q, S, Q, S, a.take<float>(n * n), true, n, n, 4 * n, 1, st, status));
+    CK(mx4_gemm(Q, S, Q, S, a.take<float>(n * n), true, n, n, 4 * n, 1, st, {status, 1}));
   } else if (which == SHP_SELFTEST_OZAKI) {
     const OzSlices sa = carve_slices(a, n, n, 1, true, false);
     const OzSlices sb = carve_slices(a, n, n, 1, false, true);
@@ -1076,7 +1105,7 @@ int shp_selftest_bounded_wait(int which, int32_t* status, float* alpha_out, void
     CK(alpha_solve(V, n, p, 1, 1, 0.5f, 1.f, 0, nullptr, alpha, nullptr, nullptr, 0, 0, nullptr,
                    st, nullptr, status));
   }
-  if (a.used > SHP_SELFTEST_WS_BYTES - kAlign) return SHP_EUNSUPPORTED;  // cannot happen
+  if (a.used > need - kAlign) return SHP_EUNSUPPORTED;  // cannot happen
   return SHP_OK;
 }
 

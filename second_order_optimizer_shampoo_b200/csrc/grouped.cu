@@ -128,7 +128,7 @@ struct RowWalk {
   TileFeed feed;
   RowTile own;
   bool have, first = true;
-  SHP_DEV RowWalk(TileSlots* ts, volatile int* abort_flag) : feed{ts, abort_flag}, have(false) {}
+  SHP_DEV RowWalk(TileSlots* ts, volatile WaitState* ws) : feed{ts, ws}, have(false) {}
   SHP_DEV bool next(RowTile& x) {
     if (first) {
       first = false;
@@ -171,7 +171,7 @@ struct RowsParams {
   int w_chunks;  // W [K][N] is mapped as 64-column chunks: both of a CTA in one box
   int dynamic;   // tiles are handed out; else taken in turn
   void* out;
-  int* status;   // bounded-wait self-test: receives SHP_ETIMEOUT (else null)
+  SelfTest test;
 };
 
 // What a tile's sums become: bf16 of one accumulator, bf16 or fp32 of summed chunks.
@@ -213,9 +213,9 @@ __global__ void __launch_bounds__(RowsCfg<NT, OUT == OUT_F32>::THREADS, 1)
   uint64_t* acce = accf + 2;
   uint64_t* drain = acce + 2;  // all MMAs of this pair complete
   uint64_t* never = drain + 1;  // completed by nothing: the self-test's wait
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(never + 1);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1) + 1;
-  static_assert((2 * STAGES + 6) * 8 + 8 <= 320, "barriers");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1);
+  volatile WaitState* ws = reinterpret_cast<volatile WaitState*>(never + 2);
+  static_assert((2 * STAGES + 7) * 8 + sizeof(WaitState) <= 320, "barriers");
 
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(RowsCfg<NT, OUT == OUT_F32>::THREADS, 1)
     mbar_init(never, 1);
     // consumers: producer and epilogue warps of both CTAs, MMA warp
     tile_slots_init(slots, 2 * (EPI_WARPS + 1) + 1);
-    *abort_flag = 0;
+    wait_state_init(ws, p.test.limit, KB);
     fence_barrier_init();
     tma_prefetch_desc(&tW);
     tma_prefetch_desc(&tX);
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(RowsCfg<NT, OUT == OUT_F32>::THREADS, 1)
   }
   if (warp == 1) tmem_alloc_pair(tmem_slot, 2 * NT);
   RowTiles<NT> tiles(p.g, p.N);
-  RowWalk walk(slots, abort_flag);
+  RowWalk walk(slots, ws);
   RowTile x;
   const int turn = static_cast<int>(blockIdx.x) / 2;
   walk.have = tiles.find(turn, walk.own);
@@ -256,7 +256,6 @@ __global__ void __launch_bounds__(RowsCfg<NT, OUT == OUT_F32>::THREADS, 1)
     RingPos<STAGES> ring;
     const uint32_t stages = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty);
     const uint32_t fleader = uniform(mapa_shared(full0, 0));
-    int landing = 0;  // an abort flag of its own for the last wait
     bool stop = false;
     while (!stop && walk.next(x)) {
       const int n0 = x.n0 + static_cast<int>(rank) * 128;
@@ -267,7 +266,7 @@ __global__ void __launch_bounds__(RowsCfg<NT, OUT == OUT_F32>::THREADS, 1)
       const int boxes = (half + 31) / 32;
       const uint32_t tx = 2 * (A_BYTES + (small ? boxes * 4096u : C::X_BYTES));
       for (int k0 = 0; k0 < p.K; k0 += BK) {
-        if (!issue_wait(empty0 + ring.slot * 8, ring.parity ^ 1u, abort_flag)) {
+        if (!issue_wait(empty0 + ring.slot * 8, ring.parity ^ 1u, ws)) {
           stop = true;
           break;
         }
@@ -295,10 +294,10 @@ __global__ void __launch_bounds__(RowsCfg<NT, OUT == OUT_F32>::THREADS, 1)
     // no MMA waits for it (the leader's barriers count the peer's copies too)
     if (leader) {
       for (int k = 0; k < STAGES; ++k, ring.advance())
-        ring_wait(full0 + ring.slot * 8, ring.parity ^ 1u, &landing);
+        mbar_wait(&full[ring.slot], ring.parity ^ 1u, nullptr, ws->limit);
     }
   } else if (warp == 1) {
-    const bool gave_up = selftest_wait(p.status, never, abort_flag);
+    const bool gave_up = selftest_wait(p.test.stall, never, &ws->abort);
     if (leader) {
       // ---------------- MMA issuer (leader of the pair)
       const uint32_t on = elect_one();
@@ -315,14 +314,14 @@ __global__ void __launch_bounds__(RowsCfg<NT, OUT == OUT_F32>::THREADS, 1)
         const uint32_t idesc = instr_desc(1u, W_MN, false, 256, (x.count + 15) & ~15);
         for (int c0 = 0; c0 < KB && !stop; c0 += CHUNKS ? CHUNK : KB, au.advance()) {
           const int c1 = CHUNKS ? min(c0 + CHUNK, KB) : KB;
-          if (!issue_wait(acce0 + au.slot * 8, au.parity ^ 1u, abort_flag)) {
+          if (!issue_wait(acce0 + au.slot * 8, au.parity ^ 1u, ws)) {
             stop = true;
             break;
           }
           tc_fence_after();
           const uint32_t dacc = tmem + au.slot * NT;
           for (int kb = c0; kb < c1; ++kb) {
-            if (!issue_wait(full0 + ring.slot * 8, ring.parity, abort_flag)) {
+            if (!issue_wait(full0 + ring.slot * 8, ring.parity, ws)) {
               stop = true;
               break;
             }
@@ -353,7 +352,7 @@ __global__ void __launch_bounds__(RowsCfg<NT, OUT == OUT_F32>::THREADS, 1)
             v[3] = x.n0;
             return true;
           },
-          abort_flag);
+          ws);
   } else {
     // ---------------- epilogue warps (both CTAs, each on its TMEM rows): warp
     // (q, h) takes the W columns of lane quarter q and the 32-row chunks
@@ -386,7 +385,7 @@ __global__ void __launch_bounds__(RowsCfg<NT, OUT == OUT_F32>::THREADS, 1)
         for (int j = 0; j < NC * 32; ++j) acc[j] = 0.f;
         for (int c0 = 0; c0 < KB; c0 += CHUNK, ++it) {
           const int u = it & 1;
-          if (!warp_wait(smem_u32(&accf[u]), (it >> 1) & 1, abort_flag)) {
+          if (!warp_wait(smem_u32(&accf[u]), (it >> 1) & 1, ws)) {
             stop = true;
             break;
           }
@@ -437,7 +436,7 @@ __global__ void __launch_bounds__(RowsCfg<NT, OUT == OUT_F32>::THREADS, 1)
         }
       } else {
         const int u = it & 1;
-        if (!warp_wait(smem_u32(&accf[u]), (it >> 1) & 1, abort_flag)) break;
+        if (!warp_wait(smem_u32(&accf[u]), (it >> 1) & 1, ws)) break;
         ++it;
         tc_fence_after();
 #pragma unroll 1
@@ -457,10 +456,11 @@ __global__ void __launch_bounds__(RowsCfg<NT, OUT == OUT_F32>::THREADS, 1)
     }
   }
 
-  // every MMA has completed (bounded; suspended, as the peer's warp waits all along)
-  if (warp == 1) warp_wait(smem_u32(drain), 0, abort_flag);
   tc_fence_before();
-  __syncthreads();
+  __syncthreads();  // every role of this CTA has left its loop
+  // so the pair's MMAs have only to complete, which a limit of a stage bounds
+  if (warp == 1) mbar_wait(drain, 0, nullptr, ws->limit);
+  selftest_report(p.test.status, &ws->abort);
   // releasing: this CTA's arrivals on the other's barriers land before it exits
   cluster_sync();
   if (warp == 1) tmem_dealloc_pair(tmem, 2 * NT);
@@ -514,7 +514,7 @@ struct WgradParams {
   int chunks;   // A and B are mapped as 64-column chunks: both of a CTA in one box
   int sorted;   // the largest groups' tiles first
   int dynamic;  // tiles are handed out; else taken in turn
-  int* status;  // bounded-wait self-test: receives SHP_ETIMEOUT (else null)
+  SelfTest test;
 };
 
 // One tile: group e, tile (m0, n0), kb stages from row k0; `tail` valid rows in
@@ -535,8 +535,8 @@ struct Walk {
   int tiles_n, per_e;
   bool first = true;
   Tile own;
-  SHP_DEV Walk(const WgradParams& q, const uint16_t* o, TileSlots* ts, volatile int* abort_flag)
-      : p(q), order(o), feed{ts, abort_flag} {
+  SHP_DEV Walk(const WgradParams& q, const uint16_t* o, TileSlots* ts, volatile WaitState* ws)
+      : p(q), order(o), feed{ts, ws} {
     tiles_n = (q.N + BN - 1) / BN;
     per_e = tiles_n * ((q.M + 255) / 256);
   }
@@ -595,10 +595,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* clearb = tailb + STAGES;  // per stage (leader): the peer's half is cleared
   uint64_t* drain = clearb + STAGES;  // all MMAs of this pair complete
   uint64_t* never = drain + 1;        // completed by nothing: the self-test's wait
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(never + 1);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1) + 1;
-  uint16_t* order = reinterpret_cast<uint16_t*>(never + 2);
-  static_assert((4 * STAGES + 6) * 8 + 8 <= 320, "barriers");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1);
+  volatile WaitState* ws = reinterpret_cast<volatile WaitState*>(never + 2);
+  uint16_t* order = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(full) + 320);
+  static_assert((4 * STAGES + 7) * 8 + sizeof(WaitState) <= 320, "barriers");
   const bool sorted = p.sorted != 0;
 
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init(never, 1);
     // consumers: producer, epilogue and clearing warps of both CTAs, MMA warp
     tile_slots_init(slots, 2 * (EPI_WARPS + 2) + 1);
-    *abort_flag = 0;
+    wait_state_init(ws, p.test.limit, p.g.T / BK + 1);
     fence_barrier_init();
     tma_prefetch_desc(&tA);
     tma_prefetch_desc(&tB);
@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     sort_groups(p.g, order, reinterpret_cast<int*>(smem));
     fence_proxy_async_smem();  // before the copies that reuse the space
   }
-  Walk walk(p, sorted ? order : nullptr, slots, abort_flag);
+  Walk walk(p, sorted ? order : nullptr, slots, ws);
   Tile x;
   const int turn = static_cast<int>(blockIdx.x) / 2;
   if (!sorted) walk.find(turn, walk.own);
@@ -644,14 +644,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     RingPos<STAGES> ring;
     const uint32_t stages = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty);
     const uint32_t tail0 = smem_u32(tailb), fleader = uniform(mapa_shared(full0, 0));
-    int landing = 0;  // an abort flag of its own for the last wait
     bool stop = false;
     while (!stop && walk.next(x)) {
       const int m0 = x.m0 + static_cast<int>(rank) * 128;
       const int nb0 = x.n0 + static_cast<int>(rank) * 128;
       int k0 = x.k0;
       for (int l = 0; l < x.kb; ++l) {
-        if (!issue_wait(empty0 + ring.slot * 8, ring.parity ^ 1u, abort_flag)) {
+        if (!issue_wait(empty0 + ring.slot * 8, ring.parity ^ 1u, ws)) {
           stop = true;
           break;
         }
@@ -691,10 +690,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     // no MMA waits for it (the leader's barriers count the peer's copies too)
     if (leader) {
       for (int k = 0; k < STAGES; ++k, ring.advance())
-        ring_wait(full0 + ring.slot * 8, ring.parity ^ 1u, &landing);
+        mbar_wait(&full[ring.slot], ring.parity ^ 1u, nullptr, ws->limit);
     }
   } else if (warp == 1) {
-    const bool gave_up = selftest_wait(p.status, never, abort_flag);
+    const bool gave_up = selftest_wait(p.test.stall, never, &ws->abort);
     if (leader) {
       // ---------------- MMA issuer (leader of the pair)
       const uint32_t idesc = instr_desc(1u, true, true, 256, BN);
@@ -712,7 +711,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         RingPos<STAGES> tail = ring;  // where the partial stage is
         for (int kb = 0; kb < x.kb; ++kb) {
           const int c = kb % CHUNK_KB;
-          if (c == 0 && !issue_wait(acce0 + au.slot * 8, au.parity ^ 1u, abort_flag)) {
+          if (c == 0 && !issue_wait(acce0 + au.slot * 8, au.parity ^ 1u, ws)) {
             stop = true;
             break;
           }
@@ -723,7 +722,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           const bool last = kb == x.kb - 1, partial = last && x.tail != 0;
           const RingPos<STAGES> at = partial ? tail : ring;
-          if (!issue_wait(full0 + at.slot * 8, at.parity, abort_flag)) {
+          if (!issue_wait(full0 + at.slot * 8, at.parity, ws)) {
             stop = true;
             break;
           }
@@ -766,7 +765,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int nc = (x.kb + CHUNK_KB - 1) / CHUNK_KB;
       for (int c = 0; c < nc; ++c, ++it) {
         const int u = it & 1;
-        if (!warp_wait(smem_u32(&accf[u]), (it >> 1) & 1, abort_flag)) {
+        if (!warp_wait(smem_u32(&accf[u]), (it >> 1) & 1, ws)) {
           stop = true;
           break;
         }
@@ -828,7 +827,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             v[4] = x.len;
             return true;
           },
-          abort_flag);
+          ws);
   } else {
     // ---------------- clearing warp: rows behind the group in its last stage
     int kit = 0;
@@ -837,7 +836,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int s = (kit + max(x.tail_at, 0)) % STAGES;
       kit = (kit + x.kb) % STAGES;
       if (x.tail == 0) continue;
-      if (!warp_wait(smem_u32(&tailb[s]), (par >> s) & 1, abort_flag)) break;
+      if (!warp_wait(smem_u32(&tailb[s]), (par >> s) & 1, ws, true)) break;
       uint8_t* st = smem + s * STAGE_BYTES;
       const int r1 = (x.tail + 15) / 16 * 16;
       // four 64-column chunks (two of A, two of B) of 64 rows of 128 bytes
@@ -853,17 +852,18 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!leader) {
         if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&clearb[s]), 0));
       } else {
-        if (!warp_wait_cluster(smem_u32(&clearb[s]), (par >> s) & 1, abort_flag)) break;
+        if (!warp_wait_cluster(smem_u32(&clearb[s]), (par >> s) & 1, ws)) break;
         if (lane == 0) mbar_arrive(&full[s]);
       }
       par ^= 1u << s;
     }
   }
 
-  // every MMA has completed (bounded; suspended, as the peer's warp waits all along)
-  if (warp == 1) warp_wait(smem_u32(drain), 0, abort_flag);
   tc_fence_before();
-  __syncthreads();
+  __syncthreads();  // every role of this CTA has left its loop
+  // so the pair's MMAs have only to complete, which a limit of a stage bounds
+  if (warp == 1) mbar_wait(drain, 0, nullptr, ws->limit);
+  selftest_report(p.test.status, &ws->abort);
   // releasing: this CTA's arrivals on the other's barriers land before it exits
   cluster_sync();
   if (warp == 1) tmem_dealloc_pair(tmem, 2 * BN);
@@ -964,14 +964,14 @@ int rows_per_tile(int64_t T, int64_t N, int64_t groups) {
 
 cudaError_t grouped_rows(const void* X, const int64_t* offsets, const void* W, bool w_trans,
                          void* Y, int T, int K, int N, int groups, bool f32, cudaStream_t st,
-                         int* selftest) {
+                         const SelfTest& selftest) {
   RowsParams p;
   memset(&p, 0, sizeof(p));
   p.g = Groups{offsets, groups, T};
   p.N = N;
   p.K = K;
   p.out = Y;
-  p.status = selftest;
+  p.test = selftest;
   CUtensorMap w;
   const int64_t kn = static_cast<int64_t>(K) * N;
   bool ok;
@@ -994,7 +994,7 @@ cudaError_t grouped_rows(const void* X, const int64_t* offsets, const void* W, b
 
 cudaError_t grouped_wgrad(const void* A, const void* B, const int64_t* offsets, float* G, int T,
                           int M, int N, int groups, bool accumulate, cudaStream_t st,
-                          int* selftest) {
+                          const SelfTest& selftest) {
   WgradParams p;
   memset(&p, 0, sizeof(p));
   CUtensorMap a, b, o;
@@ -1018,7 +1018,7 @@ cudaError_t grouped_wgrad(const void* A, const void* B, const int64_t* offsets, 
   p.M = M;
   p.N = N;
   p.accumulate = accumulate ? 1 : 0;
-  p.status = selftest;
+  p.test = selftest;
   const int64_t tiles = static_cast<int64_t>(groups) * ((M + 255) / 256) * ((N + BN - 1) / BN);
   static std::atomic<uint64_t> done{0};
   const LaunchInfo li = launch_info(reinterpret_cast<const void*>(k_grouped_wgrad), GSMEM, done);

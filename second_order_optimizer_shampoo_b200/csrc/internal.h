@@ -388,18 +388,26 @@ struct LaunchInfo {
 };
 LaunchInfo launch_info(const void* kernel, int smem, std::atomic<uint64_t>& done);
 
+// Self-tests of the bounded waits of the kernels below: `status` (a device int)
+// is set to ST_ETIMEOUT by a block in which a wait gave up, and the result is
+// then incomplete.  stall: one wait is pointed at a barrier that nothing
+// completes.  limit: the clocks a wait may take (0: SHP_SPIN_LIMIT).
+struct SelfTest {
+  int* status = nullptr;
+  int stall = 0;
+  long long limit = 0;
+};
+
 // ---- Products of rows grouped by expert (grouped.cu); bf16 operands
 // Y[t] = X[t] W_e (W: [groups][K][N]) or X[t] W_e^T (w_trans, W: [groups][N][K])
 // for the rows t of [offsets[e], offsets[e+1]); Y is bf16, or fp32 with f32.
-// selftest (here and below): a device int that the kernel's bounded-wait
-// self-test sets to ST_ETIMEOUT; the result is then left incomplete.
 cudaError_t grouped_rows(const void* X, const int64_t* offsets, const void* W, bool w_trans,
                          void* Y, int T, int K, int N, int groups, bool f32, cudaStream_t st,
-                         int* selftest = nullptr);
+                         const SelfTest& selftest = {});
 // G[e] (M x N) = A_e^T B_e over the rows of group e, or G[e] += with accumulate.
 cudaError_t grouped_wgrad(const void* A, const void* B, const int64_t* offsets, float* G, int T,
                           int M, int N, int groups, bool accumulate, cudaStream_t st,
-                          int* selftest = nullptr);
+                          const SelfTest& selftest = {});
 uint64_t kernel_runs_grouped();
 
 // ---- Microscaled 4-bit floating point (mx4.cu; layouts in the public header)
@@ -407,13 +415,13 @@ uint64_t kernel_runs_grouped();
 // along the columns (Q, S) and / or of X^T in blocks along the rows (Qt, St).
 cudaError_t mx4_quantize(const void* X, bool bf16, int rows, int cols, int64_t batch, uint8_t* Q,
                          uint8_t* S, uint8_t* Qt, uint8_t* St, cudaStream_t st,
-                         int* selftest = nullptr);
+                         const SelfTest& selftest = {});
 cudaError_t mx4_dequantize(const uint8_t* Q, const uint8_t* S, int rows, int cols, int64_t batch,
                            void* X, bool bf16, cudaStream_t st);
 // C[b] (M x N) = A[b] (M x K) B[b]^T (N x K), K a multiple of 32.
 cudaError_t mx4_gemm(const uint8_t* A, const uint8_t* As, const uint8_t* B, const uint8_t* Bs,
                      void* C, bool f32, int M, int N, int K, int64_t batch, cudaStream_t st,
-                     int* selftest = nullptr);
+                     const SelfTest& selftest = {});
 uint64_t kernel_runs_mx4();
 
 

@@ -90,7 +90,7 @@ struct QParams {
   int tiles_r, tiles_c;
   int64_t tiles;
   uint8_t* s[2];  // scale tiles per orientation (null: not wanted)
-  int* status;    // bounded-wait self-test: receives SHP_ETIMEOUT (else null)
+  SelfTest test;
 };
 
 SHP_DEV void bulk_store(void* dst, const void* src, uint32_t bytes) {
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(QTHREADS + 32, 1)
     const uint8_t* tile = smem + s * C::TILE;
     // a wait that gives up is acted on behind the barrier below, by all warps
     // together (only consumers set the flag)
-    if (it == 0) selftest_wait(p.status, never, abort_flag);
+    if (it == 0) selftest_wait(p.test.stall, never, abort_flag);
     if (!mbar_wait(&full[s], (it / C::STAGES) & 1)) *abort_flag = 1;
     uint32_t q[2][4], sb[2];
     if (p.s[0] != nullptr) {
@@ -227,6 +227,7 @@ __global__ void __launch_bounds__(QTHREADS + 32, 1)
     }
   }
   if (threadIdx.x == 0) bulk_wait_all();
+  selftest_report(p.test.status, abort_flag);
 }
 
 // Two codes (one byte of `w`) as fp32.
@@ -410,7 +411,7 @@ struct Mx4Params {
   int tiles_m, tiles_n;
   int64_t batch;
   int rb_a, rb_b;  // 128-row scale tiles per matrix of A and B
-  int* status;     // bounded-wait self-test: receives SHP_ETIMEOUT (else null)
+  SelfTest test;
 };
 
 // What a tile's sums become: bf16 of one accumulator, bf16 or fp32 of summed chunks.
@@ -443,8 +444,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* acce = accf + 2;        // shared columns drained, and all of the accumulator before
   uint64_t* drain = acce + 1;
   uint64_t* never = drain + 1;  // completed by nothing: the self-test's wait
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(never + 1);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1) + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1);
+  volatile WaitState* ws = reinterpret_cast<volatile WaitState*>(never + 2);
+  static_assert((2 * STAGES + 6) * 8 + sizeof(WaitState) <= 256, "barriers");
 
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -457,7 +459,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init(acce, 2 * EPI_WARPS);
     mbar_init(drain, 1);
     mbar_init(never, 1);
-    *abort_flag = 0;
+    wait_state_init(ws, p.test.limit, 0);
     fence_barrier_init();
     tma_prefetch_desc(&tA);
     tma_prefetch_desc(&tAs);
@@ -487,7 +489,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int za = b * p.rb_a + tm * 2 + static_cast<int>(rank);
       const int zb = b * p.rb_b + tn * NB / 128;
       for (int kb = 0; kb < KB; ++kb) {
-        if (!issue_wait(empty0 + ring.slot * 8, ring.parity ^ 1u, abort_flag)) {
+        if (!issue_wait(empty0 + ring.slot * 8, ring.parity ^ 1u, ws)) {
           stop = true;
           break;
         }
@@ -503,13 +505,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     // no copy may be in flight when the CTAs exit, also where a wait gave up and
     // no MMA waits for it (the leader's barriers count the peer's copies too)
-    int landing = 0;  // an abort flag of its own for this wait
     if (leader) {
       for (int k = 0; k < STAGES; ++k, ring.advance())
-        ring_wait(full0 + ring.slot * 8, ring.parity ^ 1u, &landing);
+        mbar_wait(&full[ring.slot], ring.parity ^ 1u, nullptr, ws->limit);
     }
   } else if (warp == 1) {
-    const bool gave_up = selftest_wait(p.status, never, abort_flag);
+    const bool gave_up = selftest_wait(p.test.stall, never, &ws->abort);
     if (leader) {
       // ---------------- MMA issuer (leader of the pair)
       const uint32_t on = elect_one();
@@ -525,14 +526,14 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int t = cl; t < ntiles && !stop; t += ncl) {
         for (int c0 = 0; c0 < KB && !stop; c0 += CHUNKS ? CHUNK : KB, u ^= 1u, pe ^= 1u) {
           const int c1 = CHUNKS ? min(c0 + CHUNK, KB) : KB;
-          if (!issue_wait(acce0, pe, abort_flag)) {
+          if (!issue_wait(acce0, pe, ws)) {
             stop = true;
             break;
           }
           tc_fence_after();
           const uint32_t dacc = tmem + u * ACC1;
           for (int kb = c0; kb < c1; ++kb) {
-            if (!ready && !issue_wait(full0 + ring.slot * 8, ring.parity, abort_flag)) {
+            if (!ready && !issue_wait(full0 + ring.slot * 8, ring.parity, ws)) {
               stop = true;
               break;
             }
@@ -609,7 +610,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int j = 0; j < NB / 2; ++j) acc[j] = 0.f;
         for (int kc = 0; kc < KB; kc += CHUNK, ++it) {
           const int u = it & 1;
-          if (!warp_wait(smem_u32(&accf[u]), (it >> 1) & 1, abort_flag)) {
+          if (!warp_wait(smem_u32(&accf[u]), (it >> 1) & 1, ws)) {
             stop = true;
             break;
           }
@@ -659,7 +660,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       } else {
         const int u = it & 1;
-        if (!warp_wait(smem_u32(&accf[u]), (it >> 1) & 1, abort_flag)) break;
+        if (!warp_wait(smem_u32(&accf[u]), (it >> 1) & 1, ws)) break;
         ++it;
         tc_fence_after();
 #pragma unroll
@@ -684,10 +685,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
   }
 
-  // every MMA has completed (bounded; suspended, as the peer's warp waits all along)
-  if (warp == 1) warp_wait(smem_u32(drain), 0, abort_flag);
   tc_fence_before();
-  __syncthreads();
+  __syncthreads();  // every role of this CTA has left its loop
+  // so the pair's MMAs have only to complete, which a limit of a stage bounds
+  if (warp == 1) mbar_wait(drain, 0, nullptr, ws->limit);
+  selftest_report(p.test.status, &ws->abort);
   // releasing: this CTA's arrivals on the other's barriers land before it exits
   cluster_sync();
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
@@ -717,9 +719,9 @@ cudaError_t launch_quantize(const CUtensorMap& x, const CUtensorMap& q, const CU
 
 cudaError_t mx4_quantize(const void* X, bool bf16, int rows, int cols, int64_t batch, uint8_t* Q,
                          uint8_t* S, uint8_t* Qt, uint8_t* St, cudaStream_t st,
-                         int* selftest) {
+                         const SelfTest& selftest) {
   QParams p;
-  p.status = selftest;
+  p.test = selftest;
   p.tiles_r = static_cast<int>(ceil_div(rows, QT));
   p.tiles_c = static_cast<int>(ceil_div(cols, QT));
   p.tiles = batch * p.tiles_r * p.tiles_c;
@@ -808,10 +810,10 @@ cudaError_t dispatch_gemm(const uint8_t* A, const uint8_t* As, const uint8_t* B,
 
 cudaError_t mx4_gemm(const uint8_t* A, const uint8_t* As, const uint8_t* B, const uint8_t* Bs,
                      void* C, bool f32, int M, int N, int K, int64_t batch, cudaStream_t st,
-                     int* selftest) {
+                     const SelfTest& selftest) {
   Mx4Params p;
   memset(&p, 0, sizeof(p));
-  p.status = selftest;
+  p.test = selftest;
   p.M = M;
   p.N = N;
   p.K = K;

@@ -97,14 +97,34 @@ SHP_DEV uint32_t mbar_try_wait_long(uint32_t addr, uint32_t parity) {
   return ok;
 }
 
+// What the bounded waits of a CTA share, in shared memory.  `limit` is for a wait
+// that ends with one step of a pipeline (a ring's stage, a chunk of an
+// accumulator), however long the launch; `tile_limit` for one that spans whole
+// tiles (the next tile's description, a stage that comes late in a tile), whose
+// length follows the work: TILE_PATIENCE clocks more for each stage of the
+// longest tile, hundreds of times what one takes (two tiles may pass during such
+// a wait), so that no accepted size runs into it.
+struct WaitState {
+  int abort;  // set by the wait that gave up; the others then give up too
+  long long limit, tile_limit;
+};
+constexpr long long TILE_PATIENCE = 1 << 18;
+
+// By one thread, before the block's first barrier.  `limit` 0: the usual one.
+SHP_DEV void wait_state_init(volatile WaitState* ws, long long limit, int64_t tile_stages) {
+  ws->abort = 0;
+  ws->limit = limit > 0 ? limit : SHP_SPIN_LIMIT;
+  ws->tile_limit = (limit > 0 ? limit : SHP_SPIN_LIMIT) + tile_stages * TILE_PATIENCE;
+}
+
 // Bounded wait by shared address; the abort flag is looked at only when the
 // phase is not complete yet, and set on giving up.
-SHP_DEV bool ring_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+SHP_DEV bool ring_wait(uint32_t bar, uint32_t parity, volatile WaitState* ws, bool tile = false) {
   if (mbar_try_wait_long(bar, parity)) return true;
   const long long t0 = clock64();
   while (!mbar_try_wait_long(bar, parity)) {
-    if (*abort_flag || clock64() - t0 > SHP_SPIN_LIMIT) {
-      *abort_flag = 1;
+    if (ws->abort || clock64() - t0 > (tile ? ws->tile_limit : ws->limit)) {
+      ws->abort = 1;
       return false;
     }
   }
@@ -112,8 +132,8 @@ SHP_DEV bool ring_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) 
 }
 // A whole warp waits; false for every lane if one lane's wait gave up, so that
 // the warp leaves its loop together.
-SHP_DEV bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  return __all_sync(0xffffffffu, ring_wait(bar, parity, abort_flag));
+SHP_DEV bool warp_wait(uint32_t bar, uint32_t parity, volatile WaitState* ws, bool tile = false) {
+  return __all_sync(0xffffffffu, ring_wait(bar, parity, ws, tile));
 }
 
 // The same wait for the loops that issue copies or MMAs, with every branch on a
@@ -121,12 +141,12 @@ SHP_DEV bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) 
 // warp-uniform issue below).  Measured: a stage of the 4-bit product (10
 // instructions, 128-column tiles) 290 -> 203 ns; 1 row over 8 groups, 4096 x 4096
 // 15.6 -> 14.4 us.  In the scheduler warp the same form costs (14.4 -> 20 us).
-SHP_DEV bool issue_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+SHP_DEV bool issue_wait(uint32_t bar, uint32_t parity, volatile WaitState* ws) {
   if (__all_sync(0xffffffffu, mbar_try_wait_long(bar, parity))) return true;
   const long long t0 = clock64();
   while (!__all_sync(0xffffffffu, mbar_try_wait_long(bar, parity))) {
-    if (__any_sync(0xffffffffu, *abort_flag || clock64() - t0 > SHP_SPIN_LIMIT)) {
-      *abort_flag = 1;
+    if (__any_sync(0xffffffffu, ws->abort || clock64() - t0 > ws->limit)) {
+      ws->abort = 1;
       return false;
     }
   }
@@ -148,8 +168,8 @@ SHP_DEV bool warp_test(uint32_t bar, uint32_t parity) {
 }
 
 // warp_wait that also acquires what the other CTA of the pair released.
-SHP_DEV bool warp_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  bool ok = ring_wait(bar, parity, abort_flag);
+SHP_DEV bool warp_wait_cluster(uint32_t bar, uint32_t parity, volatile WaitState* ws) {
+  bool ok = ring_wait(bar, parity, ws);
   if (ok) {
     uint32_t done;
     asm volatile(
@@ -168,14 +188,17 @@ SHP_DEV bool warp_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abor
 // completes (about 10 ms): long enough to be a real wait, short for a test.
 #define SHP_SELFTEST_LIMIT (20000000LL)
 
-// Bounded-wait self-test of a kernel (status non-null): waits on a barrier that
-// nothing completes, records the timeout and raises the block's abort flag.
-// True if it did.
-SHP_DEV bool selftest_wait(int* status, uint64_t* never, volatile int* abort_flag) {
-  if (status == nullptr || mbar_wait(never, 0, nullptr, SHP_SELFTEST_LIMIT)) return false;
+// Bounded-wait self-test of a kernel (stall): waits on a barrier that nothing
+// completes and raises the block's abort flag.  True if it did.
+SHP_DEV bool selftest_wait(int stall, uint64_t* never, volatile int* abort_flag) {
+  if (stall == 0 || mbar_wait(never, 0, nullptr, SHP_SELFTEST_LIMIT)) return false;
   *abort_flag = 1;
-  atomicExch(status, 19);  // SHP_ETIMEOUT
   return true;
+}
+// Its end: a block whose abort flag is up records the timeout (status null:
+// an ordinary launch, which has none).
+SHP_DEV void selftest_report(int* status, volatile const int* abort_flag) {
+  if (status != nullptr && threadIdx.x == 0 && *abort_flag) atomicExch(status, 19);  // SHP_ETIMEOUT
 }
 
 SHP_DEV void mbar_arrive(uint64_t* bar) {
@@ -528,12 +551,12 @@ SHP_DEV void tile_slots_init(TileSlots* ts, int consumers) {
 // dropped.  Every wait is bounded.
 template <class Find>
 SHP_DEV void schedule_tiles(TileSlots* ts, bool handed_out, int t, int step, Find find,
-                            volatile int* abort_flag) {
+                            volatile WaitState* ws) {
   const int lane = threadIdx.x & 31;
   RingPos<2> at;
   uint32_t asked = 0;
   for (;;) {
-    if (!warp_wait(smem_u32(&ts->empty[at.slot]), at.parity ^ 1u, abort_flag)) return;
+    if (!warp_wait(smem_u32(&ts->empty[at.slot]), at.parity ^ 1u, ws, true)) return;
     int v[8] = {-1, 0, 0, 0, 0, 0, 0, 0};
     if (handed_out) {
       do {
@@ -541,7 +564,7 @@ SHP_DEV void schedule_tiles(TileSlots* ts, bool handed_out, int t, int step, Fin
           mbar_arrive_expect_tx(&ts->asked, 16);
           try_cancel_cluster(smem_u32(&ts->answer), smem_u32(&ts->asked));
         }
-        if (!warp_wait(smem_u32(&ts->asked), asked, abort_flag)) return;
+        if (!warp_wait(smem_u32(&ts->asked), asked, ws)) return;
         asked ^= 1u;
         t = cancelled_cta(smem_u32(&ts->answer));
         fence_proxy_async_smem();  // read before the next answer is written
@@ -565,11 +588,11 @@ SHP_DEV void schedule_tiles(TileSlots* ts, bool handed_out, int t, int step, Fin
 // lane, v[0] = -1 when there is none left (or a wait gave up).
 struct TileFeed {
   TileSlots* ts;
-  volatile int* abort_flag;
+  volatile WaitState* ws;
   RingPos<2> at;
   SHP_DEV void next(int (&v)[8]) {
     v[0] = -1;
-    if (!warp_wait(smem_u32(&ts->full[at.slot]), at.parity, abort_flag)) return;
+    if (!warp_wait(smem_u32(&ts->full[at.slot]), at.parity, ws, true)) return;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = uniform(const_cast<volatile int*>(ts->tile[at.slot])[i]);
     if ((threadIdx.x & 31) == 0)

@@ -502,16 +502,22 @@ def selftest_bounded_wait(which: str, device=None):
     or "sketch_chain", the few-block sketch's grid barrier -- or "grouped",
     "wgrad", "mx4_quantize", "mx4_matmul"); returns (status
     the kernel recorded, alpha of the sketch's fit) -- SHP_ETIMEOUT and, for
-    the sketch cases, NaN are expected."""
+    the sketch cases, NaN are expected.  "grouped_long", "wgrad_long" and
+    "mx4_matmul_long" are launches much longer than the limit of a wait, in
+    which none may run out: SHP_OK is expected."""
     code = {"gemm": A.SHP_SELFTEST_GEMM, "ozaki": A.SHP_SELFTEST_OZAKI,
             "sketch": A.SHP_SELFTEST_SKETCH, "sketch_alpha": A.SHP_SELFTEST_SKETCH_ALPHA,
             "sketch_chain": A.SHP_SELFTEST_SKETCH_CHAIN, "grouped": A.SHP_SELFTEST_GROUPED,
             "wgrad": A.SHP_SELFTEST_WGRAD, "mx4_quantize": A.SHP_SELFTEST_MX4_QUANTIZE,
-            "mx4_matmul": A.SHP_SELFTEST_MX4_MATMUL}[which]
+            "mx4_matmul": A.SHP_SELFTEST_MX4_MATMUL,
+            "grouped_long": A.SHP_SELFTEST_GROUPED_LONG,
+            "wgrad_long": A.SHP_SELFTEST_WGRAD_LONG,
+            "mx4_matmul_long": A.SHP_SELFTEST_MX4_MATMUL_LONG}[which]
     device = device or torch.device("cuda", torch.cuda.current_device())
     status = torch.full((1,), -1, dtype=torch.int32, device=device)
     alpha = torch.zeros(1, dtype=torch.float32, device=device)
-    ws = torch.empty(A.SHP_SELFTEST_WS_BYTES, dtype=torch.uint8, device=device)
+    size = A.SHP_SELFTEST_LONG_WS_BYTES if which.endswith("_long") else A.SHP_SELFTEST_WS_BYTES
+    ws = torch.empty(size, dtype=torch.uint8, device=device)
     _check(A.lib().shp_selftest_bounded_wait(code, _p(status), _p(alpha), _p(ws), ws.numel(),
                                              _stream()), "shp_selftest_bounded_wait")
     return int(status.item()), float(alpha.item())
