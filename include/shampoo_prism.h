@@ -452,10 +452,12 @@ int prism_alpha_fit_noalloc(const float* R, int64_t n, int64_t batch, const floa
  *                        reaches; no alpha is solved
  *   SHP_SELFTEST_GROUPED, SHP_SELFTEST_WGRAD, SHP_SELFTEST_MX4_MATMUL  the
  *                        grouped and 4-bit products: the MMA warp's first wait
- *                        in both CTAs of the pair, with the producers' copies
- *                        in flight (they are waited for)
+ *                        in both CTAs of the pair, which gives up about a
+ *                        microsecond after the producers began to fill rings
+ *                        shorter than the contraction (their copies are waited
+ *                        for, a partial stage's too)
  *   SHP_SELFTEST_MX4_QUANTIZE  the 4-bit quantiser: the consumers' first wait,
- *                        with the producer's copies in flight
+ *                        as early, with more tiles than the producer's ring holds
  *   SHP_SELFTEST_GROUPED_LONG, SHP_SELFTEST_WGRAD_LONG,
  *   SHP_SELFTEST_MX4_MATMUL_LONG  the other way round: launches of several long
  *                        tiles, 2 to 25 times as long as the limit of a wait (set

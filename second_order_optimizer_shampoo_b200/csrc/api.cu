@@ -988,8 +988,10 @@ int shp_selftest_bounded_wait(int which, int32_t* status, float* alpha_out, void
   CK(cudaMemsetAsync(status, 0, sizeof(int32_t), st));
   CK(cudaMemsetAsync(ws, 0, need, st));
   Arena a(reinterpret_cast<void*>((reinterpret_cast<uintptr_t>(ws) + kAlign - 1) & ~(kAlign - 1)));
-  // the long launches: 50 us per wait, where a step takes under 20
-  const SelfTest slow{status, 0, 100000};
+  // expert-layer kernels: a wait gives up about a microsecond after the producers
+  // started, and theirs 5 ms later; the long launches: 50 us per wait, where a step
+  // takes under 20
+  const SelfTest stall{status, 2000, 10000000}, slow{status, 0, 100000};
   constexpr int n = 256, p = 8;  // one 256 x 256 product (a single CTA-pair tile)
   if (which == SHP_SELFTEST_GEMM) {
     float* A = a.take<float>(n * n);
@@ -1001,16 +1003,18 @@ int shp_selftest_bounded_wait(int which, int32_t* status, float* alpha_out, void
     CK(gemm_tc(MODE_TF32, op(A, nullptr, false, n, n * n), op(B, nullptr, true, n, n * n), n, n,
                n, 1, e, st));
   } else if (which == SHP_SELFTEST_GROUPED || which == SHP_SELFTEST_WGRAD) {
-    // one group of 200 rows (its last stage is partial), one tile
+    // one group of 514 rows: K of 1024 in 16 stages, and a sum over the rows in nine,
+    // the last of them partial and loaded fifth; the rings hold nine and six
+    constexpr int T = 514;
     int64_t* off = a.take<int64_t>(2);
-    uint16_t* A = a.take<uint16_t>(n * n);
-    uint16_t* B = a.take<uint16_t>(n * n);
-    float* C = a.take<float>(n * n);
-    CK(cudaMemsetAsync(off + 1, 200, 1, st));  // offsets {0, 200}, little-endian
+    uint16_t* A = a.take<uint16_t>(T * 4 * n);
+    uint16_t* B = a.take<uint16_t>(4 * n * n);
+    float* C = a.take<float>(T * n);
+    CK(cudaMemsetAsync(off + 1, T & 255, 2, st));  // offsets {0, 0x202}, little-endian
     if (which == SHP_SELFTEST_GROUPED)
-      CK(grouped_rows(A, off, B, false, C, 200, n, n, 1, true, st, {status, 1}));
+      CK(grouped_rows(A, off, B, false, C, T, 4 * n, n, 1, true, st, stall));
     else
-      CK(grouped_wgrad(A, B, off, C, 200, n, n, 1, false, st, {status, 1}));
+      CK(grouped_wgrad(A, A, off, C, T, n, n, 1, false, st, stall));
   } else if (which == SHP_SELFTEST_GROUPED_LONG) {
     // offsets 0, 4, 0, 4, ...: every second group is the same four rows, the others are
     // empty; 20 tiles of 1024 stages for four CTA pairs
@@ -1035,14 +1039,16 @@ int shp_selftest_bounded_wait(int which, int32_t* status, float* alpha_out, void
     CK(mx4_gemm(Q, S, Q, S, a.take<uint16_t>(static_cast<size_t>(M) * M), false, M, M, K, 1, st,
                 slow));
   } else if (which == SHP_SELFTEST_MX4_QUANTIZE) {
-    uint8_t* Q = a.take<uint8_t>(shp_mx4_code_bytes(n, n, 1));
-    uint8_t* S = a.take<uint8_t>(shp_mx4_scale_bytes(n, n, 1));
-    CK(mx4_quantize(a.take<float>(n * n), false, n, n, 1, Q, S, nullptr, nullptr, st,
-                    {status, 1}));
+    // 16 tiles for one CTA, whose ring holds three
+    uint8_t* Q = a.take<uint8_t>(shp_mx4_code_bytes(4 * n, n, 1));
+    uint8_t* S = a.take<uint8_t>(shp_mx4_scale_bytes(4 * n, n, 1));
+    CK(mx4_quantize(a.take<float>(4 * n * n), false, 4 * n, n, 1, Q, S, nullptr, nullptr, st,
+                    stall));
   } else if (which == SHP_SELFTEST_MX4_MATMUL) {
-    uint8_t* Q = a.take<uint8_t>(shp_mx4_code_bytes(n, 4 * n, 1));
-    uint8_t* S = a.take<uint8_t>(shp_mx4_scale_bytes(n, 4 * n, 1));
-    CK(mx4_gemm(Q, S, Q, S, a.take<float>(n * n), true, n, n, 4 * n, 1, st, {status, 1}));
+    // 16 stages; the ring holds seven
+    uint8_t* Q = a.take<uint8_t>(shp_mx4_code_bytes(n, 16 * n, 1));
+    uint8_t* S = a.take<uint8_t>(shp_mx4_scale_bytes(n, 16 * n, 1));
+    CK(mx4_gemm(Q, S, Q, S, a.take<float>(n * n), true, n, n, 16 * n, 1, st, stall));
   } else if (which == SHP_SELFTEST_OZAKI) {
     const OzSlices sa = carve_slices(a, n, n, 1, true, false);
     const OzSlices sb = carve_slices(a, n, n, 1, false, true);

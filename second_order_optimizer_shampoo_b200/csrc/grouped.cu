@@ -129,6 +129,7 @@ struct RowWalk {
   RowTile own;
   bool have, first = true;
   SHP_DEV RowWalk(TileSlots* ts, volatile WaitState* ws) : feed{ts, ws}, have(false) {}
+  template <bool PRODUCER = false>
   SHP_DEV bool next(RowTile& x) {
     if (first) {
       first = false;
@@ -136,7 +137,7 @@ struct RowWalk {
       return have;
     }
     int v[8];
-    feed.next(v);
+    feed.next<PRODUCER>(v);
     x.e = v[0];
     x.t0 = v[1];
     x.count = v[2];
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(RowsCfg<NT, OUT == OUT_F32>::THREADS, 1)
     const uint32_t stages = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty);
     const uint32_t fleader = uniform(mapa_shared(full0, 0));
     bool stop = false;
-    while (!stop && walk.next(x)) {
+    while (!stop && walk.next<true>(x)) {
       const int n0 = x.n0 + static_cast<int>(rank) * 128;
       const int half = ((x.count + 15) & ~15) / 2;  // rows per CTA
       const int t0 = x.t0 + static_cast<int>(rank) * half;
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(RowsCfg<NT, OUT == OUT_F32>::THREADS, 1)
       const int boxes = (half + 31) / 32;
       const uint32_t tx = 2 * (A_BYTES + (small ? boxes * 4096u : C::X_BYTES));
       for (int k0 = 0; k0 < p.K; k0 += BK) {
-        if (!issue_wait(empty0 + ring.slot * 8, ring.parity ^ 1u, ws)) {
+        if (!issue_wait<true>(empty0 + ring.slot * 8, ring.parity ^ 1u, ws)) {
           stop = true;
           break;
         }
@@ -292,10 +293,8 @@ __global__ void __launch_bounds__(RowsCfg<NT, OUT == OUT_F32>::THREADS, 1)
     }
     // no copy may be in flight when the CTAs exit, also where a wait gave up and
     // no MMA waits for it (the leader's barriers count the peer's copies too)
-    if (leader) {
-      for (int k = 0; k < STAGES; ++k, ring.advance())
-        mbar_wait(&full[ring.slot], ring.parity ^ 1u, nullptr, ws->limit);
-    }
+    for (int k = 0; leader && k < STAGES; ++k, ring.advance())
+      if (!mbar_wait(&full[ring.slot], ring.parity ^ 1u, nullptr, ws->limit)) break;
   } else if (warp == 1) {
     const bool gave_up = selftest_wait(p.test.stall, never, &ws->abort);
     if (leader) {
@@ -558,6 +557,7 @@ struct Walk {
     x.tail = len % BK;
     x.tail_at = x.tail == 0 ? -1 : max(0, x.kb - 1 - TAIL_EARLY);
   }
+  template <bool PRODUCER = false>
   SHP_DEV bool next(Tile& x) {
     if (first) {
       first = false;
@@ -565,7 +565,7 @@ struct Walk {
       return true;
     }
     int v[8];
-    feed.next(v);
+    feed.next<PRODUCER>(v);
     x.e = v[0];
     x.m0 = v[1];
     x.n0 = v[2];
@@ -644,13 +644,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     RingPos<STAGES> ring;
     const uint32_t stages = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty);
     const uint32_t tail0 = smem_u32(tailb), fleader = uniform(mapa_shared(full0, 0));
+    uint32_t tails = 0, tpar = 0;  // per slot: its last use is a partial stage; tailb's next phase
     bool stop = false;
-    while (!stop && walk.next(x)) {
+    while (!stop && walk.next<true>(x)) {
       const int m0 = x.m0 + static_cast<int>(rank) * 128;
       const int nb0 = x.n0 + static_cast<int>(rank) * 128;
       int k0 = x.k0;
       for (int l = 0; l < x.kb; ++l) {
-        if (!issue_wait(empty0 + ring.slot * 8, ring.parity ^ 1u, ws)) {
+        if (!issue_wait<true>(empty0 + ring.slot * 8, ring.parity ^ 1u, ws)) {
           stop = true;
           break;
         }
@@ -659,6 +660,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           // partial stage: this CTA's halves, for the clearing warp
           const uint32_t bar = tail0 + ring.slot * 8;
           const int kt = x.k0 + (x.kb - 1) * BK;
+          tails |= 1u << ring.slot;
+          tpar ^= 1u << ring.slot;
           mbar_expect_tx_if(on, bar, STAGE_BYTES);
           if (p.chunks) {
             tma_4d_if(on, sa, &tA, bar, 0, kt, m0 >> 6, 0);
@@ -671,6 +674,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         } else {
           const uint32_t fbar = fleader + ring.slot * 8;
+          tails &= ~(1u << ring.slot);
           mbar_expect_tx_if(lead, full0 + ring.slot * 8, 2 * STAGE_BYTES);
           if (p.chunks) {
             tma_4d_pair_if(on, sa, &tA, fbar, 0, k0, m0 >> 6, 0);
@@ -687,10 +691,14 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
     // no copy may be in flight when the CTAs exit, also where a wait gave up and
-    // no MMA waits for it (the leader's barriers count the peer's copies too)
-    if (leader) {
-      for (int k = 0; k < STAGES; ++k, ring.advance())
-        mbar_wait(&full[ring.slot], ring.parity ^ 1u, nullptr, ws->limit);
+    // no MMA waits for it: partial stages land on this CTA's own barriers, the
+    // others of both CTAs on the leader's
+    for (int k = 0; k < STAGES; ++k, ring.advance()) {
+      const uint32_t s = ring.slot;
+      if ((tails >> s) & 1)
+        mbar_wait(&tailb[s], ((tpar >> s) & 1) ^ 1u, nullptr, ws->limit);
+      else if (leader)
+        mbar_wait(&full[s], ring.parity ^ 1u, nullptr, ws->limit);
     }
   } else if (warp == 1) {
     const bool gave_up = selftest_wait(p.test.stall, never, &ws->abort);

@@ -391,7 +391,8 @@ LaunchInfo launch_info(const void* kernel, int smem, std::atomic<uint64_t>& done
 // Self-tests of the bounded waits of the kernels below: `status` (a device int)
 // is set to ST_ETIMEOUT by a block in which a wait gave up, and the result is
 // then incomplete.  stall: one wait is pointed at a barrier that nothing
-// completes.  limit: the clocks a wait may take (0: SHP_SPIN_LIMIT).
+// completes, and gives up after so many clocks.  limit: the clocks a wait may
+// take (0: SHP_SPIN_LIMIT).
 struct SelfTest {
   int* status = nullptr;
   int stall = 0;

@@ -126,13 +126,15 @@ __global__ void __launch_bounds__(QTHREADS + 32, 1)
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t per_b = static_cast<int64_t>(p.tiles_r) * p.tiles_c;
+  const long long limit = p.test.limit > 0 ? p.test.limit : SHP_SPIN_LIMIT;
   if (warp == QTHREADS / 32) {
     if (lane == 0) {
       tma_prefetch_desc(&tX);
       int it = 0;
       for (int64_t t = blockIdx.x; t < p.tiles; t += gridDim.x, ++it) {
         const int s = it % C::STAGES;
-        if (it >= C::STAGES && !mbar_wait(&empty[s], ((it / C::STAGES) - 1) & 1)) break;
+        if (it >= C::STAGES && !mbar_wait(&empty[s], ((it / C::STAGES) - 1) & 1, nullptr, limit))
+          break;
         const int b = static_cast<int>(t / per_b), r = static_cast<int>(t % per_b);
         const int c0 = r % p.tiles_c * QT, r0 = r / p.tiles_c * QT;
         mbar_arrive_expect_tx(&full[s], C::TILE);
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(QTHREADS + 32, 1)
       // no copy may be in flight when the CTA exits, also where the consumers
       // gave up and do not wait for it
       for (int i = it > C::STAGES ? it - C::STAGES : 0; i < it; ++i)
-        mbar_wait(&full[i % C::STAGES], (i / C::STAGES) & 1);
+        mbar_wait(&full[i % C::STAGES], (i / C::STAGES) & 1, nullptr, limit);
     }
     return;
   }
@@ -155,7 +157,7 @@ __global__ void __launch_bounds__(QTHREADS + 32, 1)
     // a wait that gives up is acted on behind the barrier below, by all warps
     // together (only consumers set the flag)
     if (it == 0) selftest_wait(p.test.stall, never, abort_flag);
-    if (!mbar_wait(&full[s], (it / C::STAGES) & 1)) *abort_flag = 1;
+    if (!mbar_wait(&full[s], (it / C::STAGES) & 1, nullptr, limit)) *abort_flag = 1;
     uint32_t q[2][4], sb[2];
     if (p.s[0] != nullptr) {
       float x[32];
@@ -489,7 +491,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int za = b * p.rb_a + tm * 2 + static_cast<int>(rank);
       const int zb = b * p.rb_b + tn * NB / 128;
       for (int kb = 0; kb < KB; ++kb) {
-        if (!issue_wait(empty0 + ring.slot * 8, ring.parity ^ 1u, ws)) {
+        if (!issue_wait<true>(empty0 + ring.slot * 8, ring.parity ^ 1u, ws)) {
           stop = true;
           break;
         }
@@ -505,10 +507,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     // no copy may be in flight when the CTAs exit, also where a wait gave up and
     // no MMA waits for it (the leader's barriers count the peer's copies too)
-    if (leader) {
-      for (int k = 0; k < STAGES; ++k, ring.advance())
-        mbar_wait(&full[ring.slot], ring.parity ^ 1u, nullptr, ws->limit);
-    }
+    for (int k = 0; leader && k < STAGES; ++k, ring.advance())
+      if (!mbar_wait(&full[ring.slot], ring.parity ^ 1u, nullptr, ws->limit)) break;
   } else if (warp == 1) {
     const bool gave_up = selftest_wait(p.test.stall, never, &ws->abort);
     if (leader) {
@@ -710,7 +710,9 @@ cudaError_t launch_quantize(const CUtensorMap& x, const CUtensorMap& q, const CU
   static std::atomic<uint64_t> done{0};
   const LaunchInfo li = launch_info(reinterpret_cast<const void*>(kern), C::SMEM, done);
   if (li.err != cudaSuccess) return li.err;
-  const unsigned grid = static_cast<unsigned>(p.tiles < li.sms ? p.tiles : li.sms);
+  // (the self-test: one CTA, so that it has more tiles than its ring holds)
+  const int64_t ctas = p.test.stall > 0 ? 1 : li.sms;
+  const unsigned grid = static_cast<unsigned>(p.tiles < ctas ? p.tiles : ctas);
   kern<<<grid, QTHREADS + 32, C::SMEM, st>>>(x, q, qt, p);
   return cudaGetLastError();
 }

@@ -105,7 +105,7 @@ SHP_DEV uint32_t mbar_try_wait_long(uint32_t addr, uint32_t parity) {
 // longest tile, hundreds of times what one takes (two tiles may pass during such
 // a wait), so that no accepted size runs into it.
 struct WaitState {
-  int abort;  // set by the wait that gave up; the others then give up too
+  int abort;  // set by the wait that gave up; the others then give up too (but see below)
   long long limit, tile_limit;
 };
 constexpr long long TILE_PATIENCE = 1 << 18;
@@ -130,6 +130,25 @@ SHP_DEV bool ring_wait(uint32_t bar, uint32_t parity, volatile WaitState* ws, bo
   }
   return true;
 }
+// The producers' form.  What a pair's producers load is counted on the leader's
+// barriers, so both have to stop at the same stage, or the leader cannot tell when
+// the last copy has landed.  They are woken by the same commits and the same tile
+// descriptions, which end within microseconds of an abort; so a producer goes on
+// for `limit` clocks after it has seen the flag, and stops when nothing has come.
+SHP_DEV bool producer_wait(uint32_t bar, uint32_t parity, volatile WaitState* ws, bool tile) {
+  if (mbar_try_wait_long(bar, parity)) return true;
+  const long long t0 = clock64();
+  long long seen = -1;
+  while (!mbar_try_wait_long(bar, parity)) {
+    const long long t = clock64();
+    if (seen < 0 && ws->abort) seen = t;
+    if ((seen >= 0 && t - seen > ws->limit) || t - t0 > (tile ? ws->tile_limit : ws->limit)) {
+      ws->abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
 // A whole warp waits; false for every lane if one lane's wait gave up, so that
 // the warp leaves its loop together.
 SHP_DEV bool warp_wait(uint32_t bar, uint32_t parity, volatile WaitState* ws, bool tile = false) {
@@ -141,11 +160,13 @@ SHP_DEV bool warp_wait(uint32_t bar, uint32_t parity, volatile WaitState* ws, bo
 // warp-uniform issue below).  Measured: a stage of the 4-bit product (10
 // instructions, 128-column tiles) 290 -> 203 ns; 1 row over 8 groups, 4096 x 4096
 // 15.6 -> 14.4 us.  In the scheduler warp the same form costs (14.4 -> 20 us).
+// PRODUCER: for a stage of the ring, as producer_wait.
+template <bool PRODUCER = false>
 SHP_DEV bool issue_wait(uint32_t bar, uint32_t parity, volatile WaitState* ws) {
   if (__all_sync(0xffffffffu, mbar_try_wait_long(bar, parity))) return true;
   const long long t0 = clock64();
   while (!__all_sync(0xffffffffu, mbar_try_wait_long(bar, parity))) {
-    if (__any_sync(0xffffffffu, ws->abort || clock64() - t0 > ws->limit)) {
+    if (__any_sync(0xffffffffu, (!PRODUCER && ws->abort) || clock64() - t0 > ws->limit)) {
       ws->abort = 1;
       return false;
     }
@@ -186,12 +207,13 @@ SHP_DEV bool warp_wait_cluster(uint32_t bar, uint32_t parity, volatile WaitState
 
 // Limit of the wait a bounded-wait self-test points at a barrier nothing
 // completes (about 10 ms): long enough to be a real wait, short for a test.
+// (The grouped and 4-bit kernels' take SelfTest::stall clocks.)
 #define SHP_SELFTEST_LIMIT (20000000LL)
 
-// Bounded-wait self-test of a kernel (stall): waits on a barrier that nothing
-// completes and raises the block's abort flag.  True if it did.
+// Bounded-wait self-test of a kernel: waits `stall` clocks (0: no test) on a
+// barrier that nothing completes and raises the block's abort flag.  True if it did.
 SHP_DEV bool selftest_wait(int stall, uint64_t* never, volatile int* abort_flag) {
-  if (stall == 0 || mbar_wait(never, 0, nullptr, SHP_SELFTEST_LIMIT)) return false;
+  if (stall == 0 || mbar_wait(never, 0, nullptr, stall)) return false;
   *abort_flag = 1;
   return true;
 }
@@ -548,7 +570,8 @@ SHP_DEV void tile_slots_init(TileSlots* ts, int consumers) {
 // waiting clusters (handed_out) or are every `step`-th from `t`.  find(t, v)
 // describes tile t, or is false if there is no such tile: then none follows it
 // in turn, and of those handed out (a grid sized by an upper bound) it is
-// dropped.  Every wait is bounded.
+// dropped.  Every wait is bounded; the answer to a question is waited for without a
+// look at the abort flag, as it is written into this CTA's shared memory.
 template <class Find>
 SHP_DEV void schedule_tiles(TileSlots* ts, bool handed_out, int t, int step, Find find,
                             volatile WaitState* ws) {
@@ -564,7 +587,7 @@ SHP_DEV void schedule_tiles(TileSlots* ts, bool handed_out, int t, int step, Fin
           mbar_arrive_expect_tx(&ts->asked, 16);
           try_cancel_cluster(smem_u32(&ts->answer), smem_u32(&ts->asked));
         }
-        if (!warp_wait(smem_u32(&ts->asked), asked, ws)) return;
+        if (!__all_sync(0xffffffffu, mbar_wait(&ts->asked, asked, nullptr, ws->limit))) return;
         asked ^= 1u;
         t = cancelled_cta(smem_u32(&ts->answer));
         fence_proxy_async_smem();  // read before the next answer is written
@@ -590,9 +613,12 @@ struct TileFeed {
   TileSlots* ts;
   volatile WaitState* ws;
   RingPos<2> at;
+  template <bool PRODUCER>
   SHP_DEV void next(int (&v)[8]) {
     v[0] = -1;
-    if (!warp_wait(smem_u32(&ts->full[at.slot]), at.parity, ws, true)) return;
+    const uint32_t bar = smem_u32(&ts->full[at.slot]);
+    const bool ok = PRODUCER ? producer_wait(bar, at.parity, ws, true) : ring_wait(bar, at.parity, ws, true);
+    if (!__all_sync(0xffffffffu, ok)) return;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = uniform(const_cast<volatile int*>(ts->tile[at.slot])[i]);
     if ((threadIdx.x & 31) == 0)
