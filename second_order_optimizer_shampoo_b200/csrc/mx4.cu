@@ -667,8 +667,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int g = 0; g < (NB == 256 ? 2 : 1); ++g) {
           const int part = NB == 256 ? (g ^ h) * 64 : 0;
           uint32_t w[64];
-          tmem_ld64_async(trow + static_cast<uint32_t>(u * ACC1 + c0 + part), w);
-          tmem_ld_wait();
+          tmem_ld64(trow + static_cast<uint32_t>(u * ACC1 + c0 + part), w);
           if (g == 0) {
             tc_fence_before();
             __syncwarp();
