@@ -127,19 +127,6 @@ constexpr uint32_t idesc_i8(int M, int N) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// 32 lanes x 16 consecutive 32-bit columns, no wait (the caller waits once
-// for several loads).
-SHP_DEV void tmem_ld16_nowait(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-SHP_DEV void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-
 // Exponent of a row (column) maximum from the high word of |max| (the key the
 // absmax kernel reduces): e with max < 2^e, scale factor 2^-e and the weight
 // sigma = 2^e / 127.  key 0: an all-zero row (factor 0, sigma 0); a
@@ -337,12 +324,33 @@ __global__ void __launch_bounds__(256)
 constexpr int OZ_EPI_WARPS = 12;  // 4 TMEM lane quarters x 3 groups of 32 columns
 constexpr int OZ_THREADS = 32 * (2 + OZ_EPI_WARPS);
 
-SHP_DEV void tmem_ld8_nowait(uint32_t taddr, uint32_t (&r)[8]) {
+// 8 columns of each level's accumulator, behind one wait (in the same statement, so
+// that nothing that uses the registers can move in front of it).
+static_assert(OZ_S == 5, "one load per level");
+SHP_DEV void tmem_ld8_levels(uint32_t taddr, uint32_t (&l)[OZ_S][8]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7])
-      : "r"(taddr));
+      "{\n\t.reg .b32 a0, a1, a2, a3, a4;\n\t"  // every input is read before an output is written
+      "mov.b32 a0, %40;\n\t"
+      "add.u32 a1, a0, %41;\n\t"
+      "add.u32 a2, a1, %41;\n\t"
+      "add.u32 a3, a2, %41;\n\t"
+      "add.u32 a4, a3, %41;\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [a0];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [a1];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16, %17, %18, %19, %20, %21, %22, %23}, [a2];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%24, %25, %26, %27, %28, %29, %30, %31}, [a3];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%32, %33, %34, %35, %36, %37, %38, %39}, [a4];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t}"
+      : "=r"(l[0][0]), "=r"(l[0][1]), "=r"(l[0][2]), "=r"(l[0][3]), "=r"(l[0][4]),
+        "=r"(l[0][5]), "=r"(l[0][6]), "=r"(l[0][7]), "=r"(l[1][0]), "=r"(l[1][1]),
+        "=r"(l[1][2]), "=r"(l[1][3]), "=r"(l[1][4]), "=r"(l[1][5]), "=r"(l[1][6]),
+        "=r"(l[1][7]), "=r"(l[2][0]), "=r"(l[2][1]), "=r"(l[2][2]), "=r"(l[2][3]),
+        "=r"(l[2][4]), "=r"(l[2][5]), "=r"(l[2][6]), "=r"(l[2][7]), "=r"(l[3][0]),
+        "=r"(l[3][1]), "=r"(l[3][2]), "=r"(l[3][3]), "=r"(l[3][4]), "=r"(l[3][5]),
+        "=r"(l[3][6]), "=r"(l[3][7]), "=r"(l[4][0]), "=r"(l[4][1]), "=r"(l[4][2]),
+        "=r"(l[4][3]), "=r"(l[4][4]), "=r"(l[4][5]), "=r"(l[4][6]), "=r"(l[4][7])
+      : "r"(taddr), "n"(OZ_BN)
+      : "memory");
 }
 
 // Phase 1 of a tile's epilogue: this thread's row, 32 columns of the five
@@ -352,10 +360,7 @@ SHP_DEV void oz_drain(uint32_t taddr, double (&acc)[32]) {
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     uint32_t l[OZ_S][8];
-#pragma unroll
-    for (int L = 0; L < OZ_S; ++L)
-      tmem_ld8_nowait(taddr + static_cast<uint32_t>(L * OZ_BN + 8 * c), l[L]);
-    tmem_wait_ld();
+    tmem_ld8_levels(taddr + static_cast<uint32_t>(8 * c), l);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       double t = i32_to_f64(l[OZ_S - 1][j]);
