@@ -1254,24 +1254,30 @@ bool tensor_map4(CUtensorMap* m, const void* ptr, int esz, const int64_t (&dims)
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-LaunchInfo launch_info(const void* kernel, int smem, std::atomic<uint64_t>& done) {
+LaunchInfo device_info() {
   static std::atomic<int> sms[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return {e, 0};
+  if (e != cudaSuccess) return {e, 0, 0};
   int n = dev < 64 ? sms[dev].load(std::memory_order_relaxed) : 0;
   if (n == 0) {
     e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return {e, 0};
+    if (e != cudaSuccess) return {e, 0, 0};
     if (dev < 64) sms[dev].store(n, std::memory_order_relaxed);
   }
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  return {cudaSuccess, n, dev};
+}
+
+LaunchInfo launch_info(const void* kernel, int smem, std::atomic<uint64_t>& done) {
+  LaunchInfo li = device_info();
+  if (li.err != cudaSuccess) return li;
+  const uint64_t bit = li.dev < 64 ? 1ull << li.dev : 0;
   if ((done.load(std::memory_order_acquire) & bit) == 0) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return {e, 0};
+    li.err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (li.err != cudaSuccess) return li;
     done.fetch_or(bit, std::memory_order_release);
   }
-  return {cudaSuccess, n};
+  return li;
 }
 
 bool tensor_map(CUtensorMap* m, const void* ptr, int esz, int64_t inner, int64_t rows,

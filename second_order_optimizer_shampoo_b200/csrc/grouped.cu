@@ -948,8 +948,8 @@ cudaError_t dispatch_rows(const void* X, const CUtensorMap& w, bool w_mn, bool f
 // tile (fewer reads of W where groups differ: 8192 skewed rows over 64 blocks
 // of 1024 x 4096, 106 us against 116 with 128 and 145 with 64), in one round
 // the smaller (16 blocks of 4096 x 1024 with 16 rows each: 29 us against 32).
-int rows_per_tile(int64_t T, int64_t N, int64_t groups) {
-  const int64_t pairs = 74, tn = (N + 255) / 256;
+int rows_per_tile(int64_t T, int64_t N, int64_t groups, int64_t pairs) {
+  const int64_t tn = (N + 255) / 256;
   const int64_t used = groups < T ? groups : T, mean = (T + used - 1) / used;
   int best = 0;
   double best_cost = 0;
@@ -993,7 +993,9 @@ cudaError_t grouped_rows(const void* X, const int64_t* offsets, const void* W, b
     ok = tensor_map(&w, W, 2, N, K, groups, N, kn, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B);
   }
   if (!ok) return cudaErrorInvalidValue;
-  switch (rows_per_tile(T, N, groups)) {
+  const LaunchInfo li = device_info();
+  if (li.err != cudaSuccess) return li.err;
+  switch (rows_per_tile(T, N, groups, li.sms / 2)) {
     case 64: return dispatch_rows<64>(X, w, !w_trans, f32, p, T, st);
     case 128: return dispatch_rows<128>(X, w, !w_trans, f32, p, T, st);
     default: return dispatch_rows<256>(X, w, !w_trans, f32, p, T, st);

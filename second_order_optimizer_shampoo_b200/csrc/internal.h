@@ -379,13 +379,14 @@ cudaError_t oz_finish(int64_t n, int batch, const Ctl& ctl, double c_exponent, c
                       float* X_out, bool z_slots, cudaStream_t st);
 uint64_t kernel_runs_ozaki();
 
-// Launch state of a kernel that is set once per device: the opt-in to `smem`
-// bytes of dynamic shared memory (`done`: one bit per device, owned by the
-// caller, one per kernel), and the device's SM count.
+// The current device and its SM count, and launch state of a kernel that is set
+// once per device: the opt-in to `smem` bytes of dynamic shared memory (`done`:
+// one bit per device, owned by the caller, one per kernel).
 struct LaunchInfo {
   cudaError_t err;
-  int sms;
+  int sms, dev;
 };
+LaunchInfo device_info();
 LaunchInfo launch_info(const void* kernel, int smem, std::atomic<uint64_t>& done);
 
 // Self-tests of the bounded waits of the kernels below: `status` (a device int)

@@ -827,9 +827,11 @@ cudaError_t mx4_gemm(const uint8_t* A, const uint8_t* As, const uint8_t* B, cons
   // 256 x 8192 x 8192 12.4 us, not 15.7; 36 blocks of 100 x 200 x 512 5.9 us, not
   // 6.5; fp32 results gain more).  With more tiles they need more rounds (40
   // tiles, 1376 columns: 8.8 against 8.9 us; 112 tiles, 4096: 20.1 against 17.3).
-  const int64_t pairs = 74;
+  // (So a launch of these has no more tiles than pairs: no pair gets a second one.)
+  const LaunchInfo li = device_info();
+  if (li.err != cudaSuccess) return li.err;
   const int64_t wide = ceil_div(M, 256) * ceil_div(N, 256) * batch;
-  return 2 * wide <= pairs ? dispatch_gemm<128>(A, As, B, Bs, C, f32, p, st)
+  return 2 * wide <= li.sms / 2 ? dispatch_gemm<128>(A, As, B, Bs, C, f32, p, st)
                            : dispatch_gemm<256>(A, As, B, Bs, C, f32, p, st);
 }
 

@@ -32,3 +32,12 @@ def test_tensor_memory_loads_wait_in_their_own_statement(name):
         for asm in statements(f.read()):
             if "tcgen05.ld." in asm:
                 assert "tcgen05.wait::ld" in asm, asm[:200]
+
+
+@pytest.mark.parametrize("name", SOURCES)
+def test_no_choice_is_made_for_a_fixed_number_of_sms(name):
+    """Tile sizes and grids follow the device's own SM count: no constant stands in
+    for it (a default that a query overwrites is not one)."""
+    with open(os.path.join(CSRC, name)) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    assert not re.findall(r"\bconst(?:expr)?\s+\w+\s+(?:pairs|sms)\s*=\s*\d+", text)
