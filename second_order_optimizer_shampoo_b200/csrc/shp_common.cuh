@@ -188,21 +188,24 @@ SHP_DEV bool warp_test(uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, ok);
 }
 
-// warp_wait that also acquires what the other CTA of the pair released.
-SHP_DEV bool warp_wait_cluster(uint32_t bar, uint32_t parity, volatile WaitState* ws) {
-  bool ok = ring_wait(bar, parity, ws);
-  if (ok) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    ok = done != 0;
-  }
-  return __all_sync(0xffffffffu, ok);
+// Behind a wait on a phase that is complete: acquires what the other CTA of the
+// pair released (or stored by st.async) with it.
+SHP_DEV bool acquire_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+// warp_wait that does so.
+SHP_DEV bool warp_wait_cluster(uint32_t bar, uint32_t parity, volatile WaitState* ws,
+                               bool tile = false) {
+  return __all_sync(0xffffffffu,
+                    ring_wait(bar, parity, ws, tile) && acquire_cluster(bar, parity));
 }
 
 // Limit of the wait a bounded-wait self-test points at a barrier nothing
@@ -409,6 +412,14 @@ SHP_DEV void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
+// Arrival on an mbarrier of either CTA that hands back tensor memory or a tile
+// slot: the reads before it are complete (tcgen05.wait::ld and a tcgen05 fence, or
+// shuffles of the values), and no memory write has to become visible with it, so it
+// need not wait for this thread's outstanding stores as a releasing arrival does.
+SHP_DEV void mbar_arrive_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
 // Arrive once on the mbarrier at this offset in every CTA of `mask` when the
 // pair's MMAs issued so far complete.
 SHP_DEV void mma_commit_pair(uint64_t* bar, uint16_t mask) {
@@ -426,14 +437,6 @@ SHP_DEV void mma_commit_pair(uint64_t* bar, uint16_t mask) {
 // clocks per instruction, measured, which bounds kernels whose stages need
 // many.  So an issuing warp runs its loop as a whole on warp-uniform values,
 // and one elected lane (`on`) executes the instruction under a predicate.
-// Arrival on an mbarrier of either CTA that hands back tensor memory: the reads
-// before it are complete (tcgen05.wait::ld and a tcgen05 fence), and no memory
-// write has to become visible with it, so it need not wait for this thread's
-// outstanding stores as a releasing arrival does.
-SHP_DEV void mbar_arrive_relaxed(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
-}
 SHP_DEV uint32_t elect_one() {
   uint32_t r;
   asm volatile(
@@ -582,7 +585,7 @@ SHP_DEV void schedule_tiles(TileSlots* ts, bool handed_out, int t, int step, Fin
   RingPos<2> at;
   uint32_t asked = 0;
   for (;;) {
-    if (!warp_wait(smem_u32(&ts->empty[at.slot]), at.parity ^ 1u, ws, true)) return;
+    if (!warp_wait_cluster(smem_u32(&ts->empty[at.slot]), at.parity ^ 1u, ws, true)) return;
     int v[8] = {-1, 0, 0, 0, 0, 0, 0, 0};
     if (handed_out) {
       do {
@@ -621,9 +624,12 @@ struct TileFeed {
     v[0] = -1;
     const uint32_t bar = smem_u32(&ts->full[at.slot]);
     const bool ok = PRODUCER ? producer_wait(bar, at.parity, ws, true) : ring_wait(bar, at.parity, ws, true);
-    if (!__all_sync(0xffffffffu, ok)) return;
+    if (!__all_sync(0xffffffffu, ok && acquire_cluster(bar, at.parity))) return;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = uniform(const_cast<volatile int*>(ts->tile[at.slot])[i]);
+    // The shuffles have consumed what every lane read, so the slot may be written
+    // again; a releasing arrival would wait for the epilogue warps' stores besides
+    // (8192 rows over 64 blocks 99 -> 109 us, 64 gradients of 1024^2 72 -> 83).
     if ((threadIdx.x & 31) == 0)
       mbar_arrive_relaxed(mapa_shared(smem_u32(&ts->empty[at.slot]), 0));
     at.advance();
