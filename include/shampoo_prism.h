@@ -326,6 +326,10 @@ int shp_split_tf32(const float* X, int64_t count, float* hi, float* lo, shp_stre
  * group.  Operands are bf16, sums fp32; K, N, m, n are multiples of 8; T and
  * the groups' sizes are arbitrary.  groups <= 65535.  No workspace.
  *
+ * A result of these products, or of the 4-bit calls below, that shares memory
+ * with an operand or another result is refused (SHP_EINVAL): tiles are written
+ * while others are still being read.
+ *
  * These products and those of the 4-bit format below have no status to report:
  * a bounded wait inside their kernels that ran out (only a device fault can
  * cause that: a wait's limit is a second for a step of a pipeline, and grows
@@ -337,8 +341,8 @@ int shp_split_tf32(const float* X, int64_t count, float* hi, float* lo, shp_stre
  * X: [T][K] bf16; W: [groups][K][N] bf16, or with w_trans = 1 [groups][N][K]
  * (W[e]^T is applied); Y: [T][N], bf16 (out_storage = SHP_BF16) or fp32
  * (SHP_TF32).  Rows of Y outside every group are left as they were.  A row of
- * Y depends on its own row of X and its group's W alone.  Y may not alias X
- * or W.  T = 0 launches nothing. */
+ * Y depends on its own row of X and its group's W alone.  T = 0 launches
+ * nothing. */
 int shp_grouped_matmul(const void* X, const int64_t* offsets, const void* W, int w_trans, void* Y,
                        int out_storage, int64_t T, int64_t K, int64_t N, int64_t groups,
                        shp_stream stream);

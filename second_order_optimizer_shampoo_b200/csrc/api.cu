@@ -10,6 +10,7 @@
 #include "internal.h"
 #include "shampoo_prism.h"
 
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
@@ -37,6 +38,23 @@ struct Arena {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+// A buffer of an argument: its bytes as a product of sizes, which may pass 64 bits.
+struct Buf {
+  const void* p;
+  unsigned __int128 bytes;
+  Buf(const void* ptr, int64_t a, int64_t b, int64_t c = 1, int64_t d = 1)
+      : p(ptr), bytes(static_cast<unsigned __int128>(a) * b * c * d) {}
+};
+// True if `out` shares memory with one of the others (a null one has none).
+bool overlaps(const Buf& out, std::initializer_list<Buf> others) {
+  const unsigned __int128 o0 = reinterpret_cast<uintptr_t>(out.p), o1 = o0 + out.bytes;
+  for (const Buf& b : others) {
+    const unsigned __int128 b0 = reinterpret_cast<uintptr_t>(b.p), b1 = b0 + b.bytes;
+    if (out.p != nullptr && b.p != nullptr && o0 < b1 && b0 < o1) return true;
+  }
+  return false;
+}
 
 // Row and column counts whose tile coordinates stay inside 32 bits.
 constexpr int64_t kMaxRows = INT32_MAX - 1024;
@@ -498,6 +516,9 @@ int shp_grouped_matmul(const void* X, const int64_t* offsets, const void* W, int
   // tiles are numbered in 32 bits (at least 64 rows by 256 columns each)
   if ((T / 64 + groups) > INT32_MAX / 2 / ((N + 255) / 256)) return SHP_EUNSUPPORTED;
   if (T == 0) return SHP_OK;
+  if (overlaps({Y, T, N, out_storage == SHP_BF16 ? 2 : 4},
+               {{X, T, K, 2}, {W, groups, K, N, 2}, {offsets, groups + 1, 8}}))
+    return SHP_EINVAL;
   CK(grouped_rows(X, offsets, W, w_trans != 0, Y, static_cast<int>(T), static_cast<int>(K),
                   static_cast<int>(N), static_cast<int>(groups), out_storage == SHP_TF32,
                   static_cast<cudaStream_t>(stream)));
@@ -512,6 +533,8 @@ int shp_grouped_wgrad(const void* A, const void* B, const int64_t* offsets, floa
   if (!aligned16(A) || !aligned16(B) || !aligned16(G) || !aligned8(offsets)) return SHP_EINVAL;
   if (T > kMaxRows || m > kMaxRows || n > kMaxRows || groups > 65535) return SHP_EUNSUPPORTED;
   if (groups * ((m + 255) / 256) > INT32_MAX / 2 / ((n + 255) / 256)) return SHP_EUNSUPPORTED;
+  if (overlaps({G, groups, m, n, 4}, {{A, T, m, 2}, {B, T, n, 2}, {offsets, groups + 1, 8}}))
+    return SHP_EINVAL;
   CK(grouped_wgrad(A, B, offsets, G, static_cast<int>(T), static_cast<int>(m),
                    static_cast<int>(n), static_cast<int>(groups), accumulate != 0,
                    static_cast<cudaStream_t>(stream)));
@@ -539,6 +562,13 @@ int shp_mx4_quantize(const void* X, int storage, int64_t rows, int64_t cols, int
     return SHP_EINVAL;
   if (rows > kMaxRows || cols > kMaxRows || batch > INT32_MAX) return SHP_EUNSUPPORTED;
   if (batch * ((rows + 127) / 128) > INT32_MAX / ((cols + 127) / 128)) return SHP_EUNSUPPORTED;
+  const Buf x(X, batch, rows, cols, storage == SHP_BF16 ? 2 : 4);
+  const Buf q(Q, batch, rows, (cols + 31) / 32, 16), qt(Qt, batch, cols, (rows + 31) / 32, 16);
+  const Buf s(S, batch, (rows + 127) / 128, (cols + 127) / 128, 512);
+  const Buf st(St, batch, (rows + 127) / 128, (cols + 127) / 128, 512);
+  if (overlaps(q, {x, s, qt, st}) || overlaps(s, {x, qt, st}) || overlaps(qt, {x, st}) ||
+      overlaps(st, {x}))
+    return SHP_EINVAL;
   CK(mx4_quantize(X, storage == SHP_BF16, static_cast<int>(rows), static_cast<int>(cols), batch,
                   static_cast<uint8_t*>(Q), static_cast<uint8_t*>(S), static_cast<uint8_t*>(Qt),
                   static_cast<uint8_t*>(St), static_cast<cudaStream_t>(stream)));
@@ -552,6 +582,10 @@ int shp_mx4_dequantize(const void* Q, const void* S, int64_t rows, int64_t cols,
   if (!aligned16(Q) || !aligned16(S) || !aligned16(X)) return SHP_EINVAL;
   if (rows > kMaxRows || cols > kMaxRows || batch > INT32_MAX) return SHP_EUNSUPPORTED;
   if (batch * ((rows + 127) / 128) > INT32_MAX / ((cols + 127) / 128)) return SHP_EUNSUPPORTED;
+  if (overlaps({X, batch, rows, cols, storage == SHP_BF16 ? 2 : 4},
+               {{Q, batch, rows, (cols + 31) / 32, 16},
+                {S, batch, (rows + 127) / 128, (cols + 127) / 128, 512}}))
+    return SHP_EINVAL;
   CK(mx4_dequantize(static_cast<const uint8_t*>(Q), static_cast<const uint8_t*>(S),
                     static_cast<int>(rows), static_cast<int>(cols), batch, X,
                     storage == SHP_BF16, static_cast<cudaStream_t>(stream)));
@@ -570,6 +604,12 @@ int shp_mx4_matmul(const void* A, const void* A_scales, const void* B, const voi
     return SHP_EINVAL;
   if (M > kMaxRows || N > kMaxRows || K > kMaxRows || batch > 65535) return SHP_EUNSUPPORTED;
   if (batch * ((M + 127) / 128) > INT32_MAX / 2 / ((N + 127) / 128)) return SHP_EUNSUPPORTED;
+  if (overlaps({C, batch, M, N, out_storage == SHP_BF16 ? 2 : 4},
+               {{A, batch, M, K / 2},
+                {A_scales, batch, (M + 127) / 128, (K + 127) / 128, 512},
+                {B, batch, N, K / 2},
+                {B_scales, batch, (N + 127) / 128, (K + 127) / 128, 512}}))
+    return SHP_EINVAL;
   CK(mx4_gemm(static_cast<const uint8_t*>(A), static_cast<const uint8_t*>(A_scales),
               static_cast<const uint8_t*>(B), static_cast<const uint8_t*>(B_scales), C,
               out_storage == SHP_TF32, static_cast<int>(M), static_cast<int>(N),

@@ -350,7 +350,8 @@ def shp_grouped_matmul(X, offsets, W, w_trans=False, out=None, dtype=torch.bfloa
     X: [T, K] bf16, rows sorted by group; offsets: [groups + 1] int64 on the
     device; W: [groups, K, N] bf16 ([groups, N, K] with w_trans).  Y: `out`, or
     a new [T, N] tensor of `dtype` (bf16 or float32) whose rows outside every
-    group are uninitialised; in `out` those rows are left as they were."""
+    group are uninitialised; in `out`, which may not share memory with X or W,
+    those rows are left as they were."""
     st = _ready(X, offsets, W, out)
     if X.dim() != 2 or W.dim() != 3:
         raise ValueError("X is [T, K] and W [groups, K, N]")
