@@ -176,7 +176,7 @@ struct RowsParams {
 };
 
 // What a tile's sums become: bf16 of one accumulator, bf16 or fp32 of summed chunks.
-enum RowsOut { OUT_BF16, OUT_BF16_CHUNKS, OUT_F32 };
+enum RowsOut { ROWS_BF16, ROWS_BF16_CHUNKS, ROWS_F32 };
 
 template <int NT, bool F32>
 struct RowsCfg {
@@ -190,12 +190,12 @@ struct RowsCfg {
 };
 
 template <int NT, bool W_MN, RowsOut OUT>
-__global__ void __launch_bounds__(RowsCfg<NT, OUT == OUT_F32>::THREADS, 1)
+__global__ void __launch_bounds__(RowsCfg<NT, OUT == ROWS_F32>::THREADS, 1)
     k_grouped_rows(const __grid_constant__ CUtensorMap tW, const __grid_constant__ CUtensorMap tX,
                    const __grid_constant__ CUtensorMap tX32,
                    const __grid_constant__ CUtensorMap tY, RowsParams p) {
   count_kernel_run();
-  constexpr bool F32 = OUT == OUT_F32, CHUNKS = OUT != OUT_BF16;
+  constexpr bool F32 = OUT == ROWS_F32, CHUNKS = OUT != ROWS_BF16;
   constexpr int CHUNK = F32 ? CHUNK_KB : LONG_KB;
   using C = RowsCfg<NT, F32>;
   constexpr int STAGES = C::STAGES;
@@ -897,7 +897,7 @@ cudaLaunchConfig_t pair_grid(int64_t pairs, int threads, int smem, cudaStream_t 
 template <int NT, bool W_MN, RowsOut OUT>
 cudaError_t launch_rows(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& x32,
                         const CUtensorMap& y, RowsParams p, int T, cudaStream_t st) {
-  using C = RowsCfg<NT, OUT == OUT_F32>;
+  using C = RowsCfg<NT, OUT == ROWS_F32>;
   auto kern = k_grouped_rows<NT, W_MN, OUT>;
   static std::atomic<uint64_t> done{0};
   const LaunchInfo li = launch_info(reinterpret_cast<const void*>(kern), C::SMEM, done);
@@ -922,9 +922,9 @@ template <int NT, bool W_MN>
 cudaError_t dispatch_out(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& x32,
                          const CUtensorMap& y, bool f32, const RowsParams& p, int T,
                          cudaStream_t st) {
-  if (f32) return launch_rows<NT, W_MN, OUT_F32>(w, x, x32, y, p, T, st);
-  return p.K > LONG_KB * BK ? launch_rows<NT, W_MN, OUT_BF16_CHUNKS>(w, x, x32, y, p, T, st)
-                      : launch_rows<NT, W_MN, OUT_BF16>(w, x, x32, y, p, T, st);
+  if (f32) return launch_rows<NT, W_MN, ROWS_F32>(w, x, x32, y, p, T, st);
+  return p.K > LONG_KB * BK ? launch_rows<NT, W_MN, ROWS_BF16_CHUNKS>(w, x, x32, y, p, T, st)
+                      : launch_rows<NT, W_MN, ROWS_BF16>(w, x, x32, y, p, T, st);
 }
 
 template <int NT>

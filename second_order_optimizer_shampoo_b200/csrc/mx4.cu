@@ -417,7 +417,7 @@ struct Mx4Params {
 };
 
 // What a tile's sums become: bf16 of one accumulator, bf16 or fp32 of summed chunks.
-enum GemmOut { OUT_BF16, OUT_BF16_CHUNKS, OUT_F32 };
+enum GemmOut { PROD_BF16, PROD_BF16_CHUNKS, PROD_F32 };
 
 template <int NB, GemmOut OUT>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   count_kernel_run();
   using C = GCfg<NB>;
   constexpr int STAGES = C::STAGES, STAGE_BYTES = C::STAGE_BYTES;
-  constexpr bool F32 = OUT == OUT_F32, CHUNKS = OUT != OUT_BF16;
+  constexpr bool F32 = OUT == PROD_F32, CHUNKS = OUT != PROD_BF16;
   constexpr int CHUNK = F32 ? CHUNK_KB : LONG_KB;
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
@@ -760,7 +760,7 @@ template <int NB, GemmOut OUT>
 cudaError_t launch_gemm(const uint8_t* A, const uint8_t* As, const uint8_t* B, const uint8_t* Bs,
                         void* O, Mx4Params p, cudaStream_t st) {
   using C = GCfg<NB>;
-  constexpr bool F32 = OUT == OUT_F32;
+  constexpr bool F32 = OUT == PROD_F32;
   p.tiles_m = static_cast<int>(ceil_div(p.M, 256));
   p.tiles_n = static_cast<int>(ceil_div(p.N, NB));
   const int64_t kt = ceil_div(p.K, 128);
@@ -802,9 +802,9 @@ cudaError_t launch_gemm(const uint8_t* A, const uint8_t* As, const uint8_t* B, c
 template <int NB>
 cudaError_t dispatch_gemm(const uint8_t* A, const uint8_t* As, const uint8_t* B, const uint8_t* Bs,
                           void* O, bool f32, const Mx4Params& p, cudaStream_t st) {
-  if (f32) return launch_gemm<NB, OUT_F32>(A, As, B, Bs, O, p, st);
-  return p.K > LONG_KB * MK ? launch_gemm<NB, OUT_BF16_CHUNKS>(A, As, B, Bs, O, p, st)
-                            : launch_gemm<NB, OUT_BF16>(A, As, B, Bs, O, p, st);
+  if (f32) return launch_gemm<NB, PROD_F32>(A, As, B, Bs, O, p, st);
+  return p.K > LONG_KB * MK ? launch_gemm<NB, PROD_BF16_CHUNKS>(A, As, B, Bs, O, p, st)
+                            : launch_gemm<NB, PROD_BF16>(A, As, B, Bs, O, p, st);
 }
 
 }  // namespace
