@@ -189,6 +189,24 @@ struct RowsCfg {
   static constexpr int THREADS = 32 * (2 + EPI_WARPS + 1);
 };
 
+// 32 rows of a bf16 tile, from row r0 of it on: v holds this lane's column, nb + lane.
+// Lane l stores columns nb + (l & ~1), + 1 of the even (odd) rows.
+SHP_DEV void store_bf16_rows(const RowsParams& p, const RowTile& x, int r0, int nb, int lane,
+                             const float* v) {
+  const int odd = lane & 1;
+  const bool in = nb + lane < p.N;  // N is even: a pair is in or out
+  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) +
+                     static_cast<int64_t>(x.t0 + r0 + odd) * p.N + nb + lane - odd;
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) {
+    const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+    const __nv_bfloat162 w = odd ? __floats2bfloat162_rn(got, v[j + 1])
+                                 : __floats2bfloat162_rn(v[j], got);
+    if (in && r0 + j + odd < x.count)
+      *reinterpret_cast<__nv_bfloat162*>(o + static_cast<int64_t>(j) * p.N) = w;
+  }
+}
+
 template <int NT, bool W_MN, RowsOut OUT>
 __global__ void __launch_bounds__(RowsCfg<NT, OUT == ROWS_F32>::THREADS, 1)
     k_grouped_rows(const __grid_constant__ CUtensorMap tW, const __grid_constant__ CUtensorMap tX,
@@ -363,21 +381,6 @@ __global__ void __launch_bounds__(RowsCfg<NT, OUT == ROWS_F32>::THREADS, 1)
     bool stop = false;
     while (!stop && walk.next(x)) {
       const int nb = x.n0 + static_cast<int>(rank) * 128 + q * 32;  // this warp's first column
-      // bf16: lane l stores columns nb + (l & ~1), + 1 of the even (odd) rows from r0 on
-      const int odd = lane & 1;
-      const bool in = nb + lane < p.N;  // N is even: a pair is in or out
-      auto store_bf16 = [&](int r0, const float* v) {
-        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) +
-                           static_cast<int64_t>(x.t0 + r0 + odd) * p.N + nb + lane - odd;
-#pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
-          const __nv_bfloat162 w = odd ? __floats2bfloat162_rn(got, v[j + 1])
-                                       : __floats2bfloat162_rn(v[j], got);
-          if (in && r0 + j + odd < x.count)
-            *reinterpret_cast<__nv_bfloat162*>(o + static_cast<int64_t>(j) * p.N) = w;
-        }
-      };
       if (CHUNKS) {
         float acc[NC * 32];
 #pragma unroll
@@ -406,7 +409,8 @@ __global__ void __launch_bounds__(RowsCfg<NT, OUT == ROWS_F32>::THREADS, 1)
         if (!F32) {
 #pragma unroll
           for (int c = 0; c < NC; ++c)
-            if ((2 * c + h) * 32 < x.count) store_bf16((2 * c + h) * 32, acc + c * 32);
+            if ((2 * c + h) * 32 < x.count)
+              store_bf16_rows(p, x, (2 * c + h) * 32, nb, lane, acc + c * 32);
         } else if (nb < p.N) {
           uint8_t* box = boxes + (warp - 2) * EPI_BOX;
 #pragma unroll
@@ -438,11 +442,25 @@ __global__ void __launch_bounds__(RowsCfg<NT, OUT == ROWS_F32>::THREADS, 1)
         if (!warp_wait(smem_u32(&accf[u]), (it >> 1) & 1, ws)) break;
         ++it;
         tc_fence_after();
+        // store_bf16_rows, written out: called, the compiler works the row addresses out
+        // again for every 32 rows (72 registers, not 114; 8192 rows over 64 blocks of
+        // 1024 x 4096: 101.1 us, not 99.8)
+        const int odd = lane & 1;
+        const bool in = nb + lane < p.N;  // N is even: a pair is in or out
 #pragma unroll 1
         for (int r0 = h * 32; r0 < x.count; r0 += 64) {
           float v[32];
           tmem_ld32(trow + static_cast<uint32_t>(u * NT + r0), v);
-          store_bf16(r0, v);
+          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) +
+                             static_cast<int64_t>(x.t0 + r0 + odd) * p.N + nb + lane - odd;
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+            const __nv_bfloat162 w = odd ? __floats2bfloat162_rn(got, v[j + 1])
+                                         : __floats2bfloat162_rn(v[j], got);
+            if (in && r0 + j + odd < x.count)
+              *reinterpret_cast<__nv_bfloat162*>(o + static_cast<int64_t>(j) * p.N) = w;
+          }
         }
         tc_fence_before();
         __syncwarp();
