@@ -1019,8 +1019,9 @@ int shp_selftest_bounded_wait(int which, int32_t* status, float* alpha_out, void
                       which == SHP_SELFTEST_MX4_MATMUL_LONG;
   const size_t need = longer ? SHP_SELFTEST_LONG_WS_BYTES : SHP_SELFTEST_WS_BYTES;
   if (status == nullptr || ws == nullptr || ws_bytes < need) return SHP_EINVAL;
-  if (!longer && which != SHP_SELFTEST_GEMM && which != SHP_SELFTEST_OZAKI && which != SHP_SELFTEST_SKETCH &&
-      which != SHP_SELFTEST_SKETCH_ALPHA && which != SHP_SELFTEST_SKETCH_CHAIN &&
+  if (!longer && which != SHP_SELFTEST_GEMM && which != SHP_SELFTEST_OZAKI &&
+      which != SHP_SELFTEST_SKETCH && which != SHP_SELFTEST_SKETCH_ALPHA &&
+      which != SHP_SELFTEST_SKETCH_CHAIN &&
       which != SHP_SELFTEST_GROUPED && which != SHP_SELFTEST_WGRAD &&
       which != SHP_SELFTEST_MX4_QUANTIZE && which != SHP_SELFTEST_MX4_MATMUL)
     return SHP_EINVAL;

@@ -163,7 +163,7 @@ struct RowWalk {
 // partial ones directly.
 //
 // Bound and rate: tensor pipe for long groups (65536 rows over 16 groups, 4096 x
-// 1024: 368 us = 1494 TFLOP/s in a short run, 533 clocks per stage of 512), HBM
+// 1024: 361 to 381 us = 1520 to 1443 TFLOP/s in a short run, 533 clocks per stage of 512), HBM
 // for short ones (64 rows over 64 groups, 1024 x 4096: 45.7 us for 280 MB of W =
 // 6.1 TB/s).
 struct RowsParams {

@@ -623,7 +623,8 @@ struct TileFeed {
   SHP_DEV void next(int (&v)[8]) {
     v[0] = -1;
     const uint32_t bar = smem_u32(&ts->full[at.slot]);
-    const bool ok = PRODUCER ? producer_wait(bar, at.parity, ws, true) : ring_wait(bar, at.parity, ws, true);
+    const bool ok = PRODUCER ? producer_wait(bar, at.parity, ws, true)
+                             : ring_wait(bar, at.parity, ws, true);
     if (!__all_sync(0xffffffffu, ok && acquire_cluster(bar, at.parity))) return;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = uniform(const_cast<volatile int*>(ts->tile[at.slot])[i]);
