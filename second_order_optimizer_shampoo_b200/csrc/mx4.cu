@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(256)
 // Bound and rate: a stage of NB = 256 brings 35 KB into each SM for 512 clocks of
 // MMAs, 68 bytes per clock, about what the path from L2 delivers: 8192 x 8192 x
 // 4096 95 to 98 us = 5.6 to 5.8 PFLOP/s in a short run, about 550 clocks per stage;
-// under the power cap 114 to 118 us.
+// under the power cap 114 to 119 us.
 
 constexpr int MK = 256;  // codes per stage row: 128 bytes
 constexpr int CHUNK_KB = 8;   // stages per chunk of an fp32 result
